@@ -128,11 +128,16 @@ PFKV_API int pfkv_kv_append_bf16(const void *k_new, const void *v_new, void *k_c
  *   PFKV_SCALE_HEAD    [num_kv_heads]
  *   PFKV_SCALE_TOKEN   [num_pages][num_kv_heads][page_size], entry
  *                      (page * num_kv_heads + h) * page_size + offset beside
- *                      the cache row it scales */
+ *                      the cache row it scales
+ *   PFKV_SCALE_BLOCK   [num_pages][num_kv_heads]: one scale for each page and
+ *                      KV head, between per head and per token; written by
+ *                      pfkv_kv_append_fp8_block.  The pages have no
+ *                      counterpart of it. */
 typedef enum {
   PFKV_SCALE_TENSOR = 0,
   PFKV_SCALE_HEAD = 1,
-  PFKV_SCALE_TOKEN = 2
+  PFKV_SCALE_TOKEN = 2,
+  PFKV_SCALE_BLOCK = 3
 } pfkv_scale_granularity;
 
 /* kv_append_fp8_scaled -- kv_append_fp8 with device-resident scales.
@@ -147,13 +152,49 @@ typedef enum {
  * Other arguments, layouts and skipped slots as kv_append_fp8; v_new = v_cache
  * = v_scales = NULL appends K only.
  * Supported: head_dim a multiple of 16 (TOKEN: at most 512); scale arrays
- * 4-byte aligned.  Errors: PFKV_ERR_INVALID_ARG for an unknown granularity or
- * a NULL scale array, plus those of kv_append_fp8. */
+ * 4-byte aligned.  Errors: PFKV_ERR_INVALID_ARG for an unknown granularity
+ * (BLOCK too: pfkv_kv_append_fp8_block) or a NULL scale array, plus those of
+ * kv_append_fp8. */
 PFKV_API int pfkv_kv_append_fp8_scaled(const void *k_new, const void *v_new, void *k_cache,
                                        void *v_cache, const int64_t *slot_mapping, int num_tokens,
                                        int num_kv_heads, int head_dim, int page_size,
                                        int64_t num_pages, pfkv_scale_granularity granularity,
                                        float *k_scales, float *v_scales, pfkv_stream_t stream);
+
+/* kv_append_fp8_block -- new K/V rows into pages that hold one scale per
+ * (page, KV head) (PFKV_SCALE_BLOCK).  A block's scale depends on all of its
+ * rows, so this call takes whole requests instead of a slot mapping: request
+ * b's n_b = new_start[b+1] - new_start[b] new tokens are its last ones, at
+ * positions L_b - n_b .. L_b - 1, in the pages its block table names.
+ * For each page that receives new rows, each head and tensor, with a = max |x|
+ * over the new rows and need(a) the smallest power of two s >= 2^-126 with
+ * a <= 448 s:
+ *     old   = the stored scale if the page holds earlier rows of the request,
+ *             0 otherwise (the stored value is then not used)
+ *     scale = max(old, need(a))
+ *     new codes = e4m3_rne_satfinite(x / scale)
+ *     if scale > old, earlier codes c become e4m3_rne_satfinite(c old / scale)
+ * A block of zeros has scale 2^-126.  Powers of two keep both divisions exact
+ * shifts, so a scale that grows re-rounds nothing that stays a normal e4m3
+ * number, and appending the same rows twice gives the same bytes.
+ *   k_new, v_new      bf16 [num_tokens][num_kv_heads][head_dim], finite
+ *   k_cache, v_cache  e4m3 [num_pages][num_kv_heads][page_size][head_dim]
+ *   k_scales, v_scales  fp32 [num_pages][num_kv_heads], read and written; the
+ *                     scale of a page with earlier rows is one this call wrote
+ *   new_start         int32 [batch + 1] (device), non-decreasing from 0
+ *   max_new_len       host bound on every n_b (the grid is sized from it)
+ * v_new = v_cache = v_scales = NULL appends K only.  A request with n_b < 0,
+ * n_b > max_new_len, n_b > L_b, rows outside [0, num_tokens) or L_b beyond its
+ * table is left out, as is a page outside the pool; nothing else is written.
+ * A page may receive rows from one request per call (shared prefix pages are
+ * full: appends go to a request's own last pages).
+ * Supported: head_dim a multiple of 16, any page_size. */
+PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
+                                      float *k_scales, float *v_scales, const int32_t *block_tables,
+                                      int max_pages_per_seq, const int32_t *context_lens,
+                                      const int32_t *new_start, int batch, int num_tokens, int max_new_len,
+                                      int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                      pfkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* paged_decode_attn -- one decode step of GQA/MHA attention over the paged
@@ -248,7 +289,8 @@ PFKV_API int pfkv_paged_decode_attn_noalloc(void *out, const void *q, const void
  * pfkv_scale_granularity):
  *   s_t = softmax_scale * sum_d q[b][h][d] * e4m3(Kcode_t[d]) * ks(t)
  *   out = sum_t e^{s_t - m} e4m3(Vcode_t[d]) * vs(t) / sum_t e^{s_t - m}
- * with ks(t), vs(t) = scales[0], scales[kvh] or the scale stored beside row t.
+ * with ks(t), vs(t) = scales[0], scales[kvh], the scale stored beside row t, or
+ * the scale of row t's page and KV head (BLOCK).
  * Per tensor and per head, the scales fold into the score and output factors
  * of each work unit, so the tile loop is unchanged.  Per token, the 16 K and
  * 16 V scales of each 16-token tile (2 x 64 bytes) are copied in with the
@@ -257,7 +299,9 @@ PFKV_API int pfkv_paged_decode_attn_noalloc(void *out, const void *q, const void
  * the largest V scale seen so far in the work unit, multiplies its token's
  * probability before the f16 P.V product (the accumulator is rescaled when
  * that largest scale grows, as for the running maximum of the softmax).
- * Numerics: per tensor and per head as pfkv_paged_decode_attn; per token, the
+ * Per block: two loads per 16-token tile, each K scale on the tile's raw
+ * scores, V scales as weights as per token; 8 / page_size extra bytes per row.
+ * Numerics: per tensor, per head and per block as pfkv_paged_decode_attn; per token, the
  * score products are f16 on K widened in registers, against q times one
  * power of two per work unit that takes its largest |q| into (2^14, 2^15]
  * (any finite bf16 q; exact for every value at least 2^-29 of that largest).
@@ -279,6 +323,96 @@ PFKV_API int pfkv_paged_decode_attn_scaled(void *out, const void *q, const void 
                                            int kv_split_tokens, void *workspace,
                                            size_t workspace_bytes, float *lse_out,
                                            pfkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
+/* Block-sparse decode: a query attends to a few pages of its context, chosen
+ * for each (request, KV head) by a cheap score.  kLLM article, §5.1.1: only
+ * the top-k historical tokens take part in the attention; here the unit is the
+ * page and the list is made by the library.  Three calls, in a decode step
+ * after the append: pfkv_page_key_bounds brings the summaries of the pages the
+ * step touched up to date, pfkv_select_pages lists pages, and
+ * pfkv_paged_sparse_decode_attn attends to them.  None takes a workspace.
+ *
+ * unit_status (the last two calls): optional int32 [batch][num_kv_heads],
+ * device; every entry is written, 0 or an OR of PFKV_DEVERR_* bits.
+ *
+ * page_key_bounds -- channelwise bounds of the keys of every page that holds
+ * one of a request's last n_b = new_start[b+1] - new_start[b] tokens (n_b = L_b
+ * summarises a whole context; the arrays of the append fit).  For such a page
+ * and head, over its rows t < L_b, in units of the page's K scale:
+ *     lo_d = min_t K_t[d],  hi_d = max_t K_t[d],  A = max_d max(|lo_d|, |hi_d|)
+ *     s = the smallest power of two >= 2^-15 with A <= 127 s
+ *     bounds[page][h][0][d] = floor(lo_d / s)
+ *     bounds[page][h][1][d] = ceil(hi_d / s),  bound_scales[page][h] = s
+ * K codes that are NaN are passed over.
+ *   bounds        int8 [num_pages][num_kv_heads][2][head_dim], written
+ *   bound_scales  fp32 [num_pages][num_kv_heads], written
+ *   k_cache       e4m3 [num_pages][num_kv_heads][page_size][head_dim]
+ *   new_start     int32 [batch + 1] (device); max_new_len: host bound on n_b
+ * Requests and pages whose numbers do not fit are left out, as in
+ * pfkv_kv_append_fp8_block.  Supported: head_dim 128, any page_size. */
+PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
+                                  const int32_t *block_tables, int max_pages_per_seq,
+                                  const int32_t *context_lens, const int32_t *new_start, int batch,
+                                  int max_new_len, int num_kv_heads, int head_dim, int page_size,
+                                  int64_t num_pages, pfkv_stream_t stream);
+
+/* select_pages -- the top_pages pages of each (request, KV head), ascending.
+ * With G = num_q_heads / num_kv_heads query heads in the group:
+ *     n_g[d]  = rint(q_g[d] 2^(14 - e)), 2^(e-1) <= max over the group |q| < 2^e
+ *     S+[d]   = sum_g max(n_g[d], 0),  S-[d] = sum_g min(n_g[d], 0)
+ *     Q+-[d]  = rint(S+-[d] / 2^j), j >= 0 the smallest with max |S+-| <= 127 2^j
+ *     score(page) = (sum_d Q+[d] hi[d] + Q-[d] lo[d]) * bound_scale(page)
+ *                   [* k_scales(page, h)]
+ * (rint: to nearest, ties to even).  The score is the group's sum of upper
+ * bounds of q . k over the page, up to the query's rounding to 8 bits and a
+ * factor common to all pages; it is exact in fp32 while the scales are powers
+ * of two, so equal scores are ties, and ties go to the lower page.  The first
+ * sink_pages and the last recent_pages pages are listed whatever their score.
+ *   selected      int32 [batch][num_kv_heads][top_pages], written: logical
+ *                 pages t / page_size in ascending order, then -1 where the
+ *                 context has fewer than top_pages pages
+ *   q             bf16 [batch][num_q_heads][head_dim]
+ *   k_scales      the fp32 [num_pages][num_kv_heads] scales of a cache with
+ *                 scales per block; NULL for scales per tensor or head, which
+ *                 are common to all pages of a head
+ * A page outside the pool scores lowest (PFKV_DEVERR_BAD_PAGE); a length
+ * outside the table is clamped (PFKV_DEVERR_BAD_CONTEXT).
+ * Supported: head_dim 128; G in 1..16; sink_pages + recent_pages <= top_pages;
+ * max_pages_per_seq <= 393216; any page_size. */
+PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *bounds,
+                               const float *bound_scales, const float *k_scales,
+                               const int32_t *block_tables, int max_pages_per_seq,
+                               const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads,
+                               int head_dim, int page_size, int64_t num_pages, int top_pages,
+                               int sink_pages, int recent_pages, int32_t *unit_status,
+                               pfkv_stream_t stream);
+
+/* paged_sparse_decode_attn -- paged_decode_attn_scaled over listed pages only:
+ * for request b and KV head h the softmax runs over the tokens t < L_b of the
+ * pages selected[b][h][0 .. top_pages-1].
+ *   granularity   PFKV_SCALE_TENSOR, _HEAD or _BLOCK (per token: unsupported)
+ *   selected      int32 [batch][num_kv_heads][top_pages], logical pages, each at
+ *                 most once, in any order; entries < 0 are padding.  Only the
+ *                 first ceil(L_b / page_size) entries are read: a list of
+ *                 distinct pages has no more.  An entry beyond the context is
+ *                 passed over (PFKV_DEVERR_BAD_TOPK), as is a page outside the
+ *                 pool (PFKV_DEVERR_BAD_PAGE).
+ *   lse_out       optional fp32 [batch][num_q_heads]
+ * No token attended gives out = 0 and lse = -inf.  Numerics as
+ * pfkv_paged_decode_attn_scaled per block; results do not depend on what else
+ * runs, but the order of the sums follows the SM count and the sizes.
+ * Supported: as pfkv_paged_decode_attn, e4m3 cache; scale arrays 4-byte
+ * aligned. */
+PFKV_API int pfkv_paged_sparse_decode_attn(void *out, const void *q, const void *k_cache,
+                                           const void *v_cache, pfkv_scale_granularity granularity,
+                                           const float *k_scales, const float *v_scales,
+                                           const int32_t *selected, int top_pages,
+                                           const int32_t *block_tables, int max_pages_per_seq,
+                                           const int32_t *context_lens, int batch, int num_q_heads,
+                                           int num_kv_heads, int head_dim, int page_size,
+                                           int64_t num_pages, float softmax_scale, float *lse_out,
+                                           int32_t *unit_status, pfkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
 /* paged_prefill_attn -- several new query tokens per request over the paged

@@ -19,7 +19,10 @@ from . import _build
 
 __all__ = [
     "PfkvError", "load", "lib_path", "kv_append_fp8", "kv_append_bf16",
-    "paged_decode_workspace_size", "paged_decode_attn", "paged_decode_attn_noalloc",
+    "kv_append_fp8_scaled", "kv_append_fp8_block", "page_key_bounds", "select_pages", "paged_sparse_decode_attn",
+    "paged_decode_workspace_size", "paged_decode_attn", "paged_decode_attn_noalloc", "paged_decode_attn_scaled",
+    "paged_prefill_workspace_size", "paged_prefill_attn",
+    "SCALE_TENSOR", "SCALE_HEAD", "SCALE_TOKEN", "SCALE_BLOCK",
     "mla_decode_workspace_size",
     "mla_decode_attn", "validate_tables", "verify_page_tags", "workspace_status", "selftest_barrier_timeout",
     "last_error", "version",
@@ -69,6 +72,13 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "pfkv_kv_append_bf16": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, vp]),
             "pfkv_kv_append_fp8_scaled": (i32, [vp, vp, vp, vp, vp, i32, i32, i32, i32, i64, i32, vp, vp,
                                                 vp]),
+            "pfkv_kv_append_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
+                                               i32, i64, vp]),
+            "pfkv_page_key_bounds": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, vp]),
+            "pfkv_select_pages": (i32, [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, i32,
+                                        i32, vp, vp]),
+            "pfkv_paged_sparse_decode_attn": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, i32, i32,
+                                                    i32, i32, i32, i64, f32, vp, vp, vp]),
             "pfkv_paged_decode_workspace_size": (sz, [i32, i32, i32, i32, i32, i64]),
             "pfkv_paged_decode_attn": (i32, [vp, vp, vp, vp, i32, vp, i32, vp, i32, i32, i32, i32, i32,
                                              i64, f32, f32, f32, i32, vp, sz, vp, vp]),
@@ -160,6 +170,7 @@ def kv_append_bf16(k_new, v_new, k_cache, v_cache, slot_mapping, stream=None):
 SCALE_TENSOR = 0
 SCALE_HEAD = 1
 SCALE_TOKEN = 2
+SCALE_BLOCK = 3
 
 
 def kv_append_fp8_scaled(k_new, v_new, k_cache, v_cache, slot_mapping, granularity: int, k_scales,
@@ -173,6 +184,131 @@ def kv_append_fp8_scaled(k_new, v_new, k_cache, v_cache, slot_mapping, granulari
                                           _ptr(slot_mapping), T, H, D, P, pages, int(granularity),
                                           _ptr(k_scales), _ptr(v_scales), _stream(stream))
     _check("kv_append_fp8_scaled", rc)
+
+
+def _want(name: str, t, dtype, shape, device) -> int:
+    """Device address of a tensor that has to be just this; ValueError otherwise."""
+    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
+                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
+    return t.data_ptr()
+
+
+def _call(fn: str, device, stream, *args):
+    """One entry point on `device`: its current stream unless one is given."""
+    import torch
+    if device.type != "cuda":
+        raise ValueError("expected CUDA tensors")
+    if stream is None:
+        stream = torch.cuda.current_stream(device)
+    elif stream.device != device:
+        raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to {device}")
+    f = getattr(load(), "pfkv_" + fn)
+    if device.index == torch.cuda.current_device():
+        rc = f(*args, stream.cuda_stream)
+    else:
+        with torch.cuda.device(device):
+            rc = f(*args, stream.cuda_stream)
+    _check(fn, rc)
+
+
+def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, new_start,
+                        max_new_len: int, stream=None):
+    """Quantise the last n_b = new_start[b+1] - new_start[b] tokens of every
+    request (rows new_start[b].. of k_new/v_new bf16 [T][H][D]) into the pages
+    of its block table, with one power-of-two scale per (page, KV head) in
+    k_scales/v_scales float32 [pages][H]; a scale grows, and the page's earlier
+    codes move to it, when new rows need it.  context_lens int32 [B] counts the
+    new tokens; new_start int32 [B+1]; max_new_len bounds every n_b.  For K
+    alone pass v_new = v_cache = v_scales = None."""
+    import torch
+    dev = k_new.device
+    T, H, D = k_new.shape
+    pages, _, P, _ = k_cache.shape
+    B, maxp = block_tables.shape
+    cache, scales = (pages, H, P, D), (pages, H)
+    v = [None, None, None]
+    if not (v_new is None and v_cache is None and v_scales is None):
+        if v_new is None or v_cache is None or v_scales is None:
+            raise ValueError("v_new, v_cache and v_scales: all or none")
+        v = [_want("v_new", v_new, torch.bfloat16, k_new.shape, dev), _want("v_cache", v_cache, torch.uint8, cache, dev),
+             _want("v_scales", v_scales, torch.float32, scales, dev)]
+    _call("kv_append_fp8_block", dev, stream, _want("k_new", k_new, torch.bfloat16, (T, H, D), dev), v[0],
+          _want("k_cache", k_cache, torch.uint8, cache, dev), v[1],
+          _want("k_scales", k_scales, torch.float32, scales, dev), v[2],
+          _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
+          _want("context_lens", context_lens, torch.int32, (B,), dev),
+          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, T, int(max_new_len), H, D, P, pages)
+
+
+# ---------------------------------------------------------- block-sparse decode
+def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, new_start, max_new_len: int,
+                    stream=None):
+    """Channelwise bounds of the keys of every page that holds one of a
+    request's last new_start[b+1] - new_start[b] tokens: bounds int8
+    [pages][H][2][128] (lower, upper) in units of bound_scales float32
+    [pages][H] times the page's K scale, from the e4m3 k_cache uint8
+    [pages][H][P][128].  max_new_len bounds the counts."""
+    import torch
+    dev = k_cache.device
+    pages, H, P, D = k_cache.shape
+    B, maxp = block_tables.shape
+    _call("page_key_bounds", dev, stream, _want("bounds", bounds, torch.int8, (pages, H, 2, D), dev),
+          _want("bound_scales", bound_scales, torch.float32, (pages, H), dev),
+          _want("k_cache", k_cache, torch.uint8, (pages, H, P, D), dev),
+          _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
+          _want("context_lens", context_lens, torch.int32, (B,), dev),
+          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, int(max_new_len), H, D, P, pages)
+
+
+def select_pages(selected, q, bounds, bound_scales, block_tables, context_lens, page_size: int, sink_pages: int = 1,
+                 recent_pages: int = 1, k_scales=None, unit_status=None, stream=None):
+    """List the pages each (request, KV head) attends: selected int32
+    [B][Hkv][top_pages] receives logical page numbers in ascending order, -1
+    past a shorter context's last.  q bf16 [B][Hq][128]; bounds and
+    bound_scales from page_key_bounds; k_scales float32 [pages][Hkv] for a
+    cache with scales per block.  The first sink_pages and last recent_pages
+    pages are always listed.  unit_status: optional int32 [B][Hkv]."""
+    import torch
+    dev = q.device
+    B, Hq, D = q.shape
+    pages, Hkv = bound_scales.shape
+    maxp, top = block_tables.shape[1], selected.shape[2]
+    _call("select_pages", dev, stream, _want("selected", selected, torch.int32, (B, Hkv, top), dev),
+          _want("q", q, torch.bfloat16, (B, Hq, D), dev), _want("bounds", bounds, torch.int8, (pages, Hkv, 2, D), dev),
+          _want("bound_scales", bound_scales, torch.float32, (pages, Hkv), dev),
+          None if k_scales is None else _want("k_scales", k_scales, torch.float32, (pages, Hkv), dev),
+          _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
+          _want("context_lens", context_lens, torch.int32, (B,), dev), B, Hq, Hkv, D, int(page_size), pages, top,
+          int(sink_pages), int(recent_pages),
+          None if unit_status is None else _want("unit_status", unit_status, torch.int32, (B, Hkv), dev))
+
+
+def paged_sparse_decode_attn(out, q, k_cache, v_cache, granularity: int, k_scales, v_scales, selected, block_tables,
+                             context_lens, softmax_scale: float, lse_out=None, unit_status=None, stream=None):
+    """One decode step over the pages listed for each (request, KV head):
+    out/q bf16 [B][Hq][128]; caches uint8 (e4m3) [pages][Hkv][P][128]; scales
+    float32 of SCALE_TENSOR [1], SCALE_HEAD [Hkv] or SCALE_BLOCK [pages][Hkv];
+    selected int32 [B][Hkv][top_pages], as select_pages writes it (distinct
+    logical pages; entries < 0 are padding).  lse_out: optional float32
+    [B][Hq]; unit_status: optional int32 [B][Hkv]."""
+    import torch
+    dev = q.device
+    B, Hq, D = q.shape
+    pages, Hkv, P, _ = k_cache.shape
+    maxp, top = block_tables.shape[1], selected.shape[2]
+    cache = (pages, Hkv, P, D)
+    scales = {SCALE_TENSOR: (1,), SCALE_HEAD: (Hkv,), SCALE_BLOCK: (pages, Hkv)}.get(granularity, k_scales.shape)
+    _call("paged_sparse_decode_attn", dev, stream, _want("out", out, torch.bfloat16, (B, Hq, D), dev),
+          _want("q", q, torch.bfloat16, (B, Hq, D), dev), _want("k_cache", k_cache, torch.uint8, cache, dev),
+          _want("v_cache", v_cache, torch.uint8, cache, dev), int(granularity),
+          _want("k_scales", k_scales, torch.float32, scales, dev),
+          _want("v_scales", v_scales, torch.float32, scales, dev),
+          _want("selected", selected, torch.int32, (B, Hkv, top), dev), top,
+          _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
+          _want("context_lens", context_lens, torch.int32, (B,), dev), B, Hq, Hkv, D, P, pages, float(softmax_scale),
+          None if lse_out is None else _want("lse_out", lse_out, torch.float32, (B, Hq), dev),
+          None if unit_status is None else _want("unit_status", unit_status, torch.int32, (B, Hkv), dev))
 
 
 # ---------------------------------------------------------------- decode
@@ -209,10 +345,13 @@ def paged_decode_attn_scaled(out, q, k_cache, v_cache, granularity: int, k_scale
                              workspace=None, lse_out=None, stream=None, max_total_chunks: int = 0):
     """paged_decode_attn over an e4m3 cache with float32 device scales of the
     given granularity (SCALE_TENSOR [1], SCALE_HEAD [Hkv], SCALE_TOKEN
-    [pages][Hkv][P]).  Returns the workspace used."""
+    [pages][Hkv][P], SCALE_BLOCK [pages][Hkv]).  Returns the workspace used."""
     import torch
     B, Hq, D = q.shape
     pages, Hkv, P, _ = k_cache.shape
+    if granularity == SCALE_BLOCK:
+        for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
+            _want(name, t, torch.float32, (pages, Hkv), q.device)
     if workspace is None:
         n = paged_decode_workspace_size(B, Hq, Hkv, D, kv_split_tokens, max_total_chunks)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)

@@ -145,6 +145,9 @@ int append_common(bool fp8, const void* k_new, const void* v_new, void* k_cache,
       return fail(PFKV_ERR_INVALID_ARG, "kv_append_fp8: scales must be finite and > 0");
   }
   if (gran >= 0) {
+    if (gran == PFKV_SCALE_BLOCK)
+      return fail(PFKV_ERR_INVALID_ARG,
+                  "kv_append_fp8_scaled: granularity %d (per block) is written by kv_append_fp8_block", gran);
     if (gran != PFKV_SCALE_TENSOR && gran != PFKV_SCALE_HEAD && gran != PFKV_SCALE_TOKEN)
       return fail(PFKV_ERR_INVALID_ARG, "kv_append_fp8_scaled: unknown granularity %d", gran);
     if (!k_scales || (has_v && !v_scales))

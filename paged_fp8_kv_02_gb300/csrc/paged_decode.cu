@@ -57,9 +57,11 @@ constexpr int kMaxGrid = 1024;    // bound on persistent CTAs (sizes the workspa
 constexpr int kMaxWarps = kMaxGrid * kWarps;
 constexpr float kLog2e = 1.4426950408889634f;
 // Where the K/V scales come from: host scalars in DecodeArgs, one device scale
-// per work unit (per tensor or per KV head), or one per token row.
-enum : int { kSclHost = 0, kSclUnit = 1, kSclToken = 2 };
+// per work unit (per tensor or per KV head), one per token row, or one per
+// (page, KV head).
+enum : int { kSclHost = 0, kSclUnit = 1, kSclToken = 2, kSclBlock = 3 };
 constexpr int kScaleStageBytes = 128;  // per-token mode: 16 K + 16 V fp32 scales per stage
+constexpr int kBlockScaleBytes = 8;    // per-block mode: the tile's K and V scale
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeArgs {
@@ -220,7 +222,8 @@ struct Geometry {
   static constexpr int kStageBytes = 2 * kKBytes;       // K + V
   static constexpr int kWarpBytes = kStages * kStageBytes;
   // per-token scales sit after all warps' tiles (which keep their 1024-byte alignment)
-  static constexpr int kScaleWarpBytes = kScl == kSclToken ? kStages * kScaleStageBytes : 0;
+  static constexpr int kScaleWarpBytes =
+      kScl == kSclToken ? kStages * kScaleStageBytes : (kScl == kSclBlock ? kStages * kBlockScaleBytes : 0);
   static constexpr int kSmemBytes = kWarps * (kWarpBytes + kScaleWarpBytes) + 1024;  // + alignment slack
 };
 
@@ -247,7 +250,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
   const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
   const uint32_t wbase = smem_base + warp * Geo::kWarpBytes;
   uint8_t* const wptr = smem_raw + (smem_base - smem_u32(smem_raw)) + warp * Geo::kWarpBytes;
-  // per-token mode: this warp's kStages x (16 K + 16 V) fp32 scales
+  // per-token mode: this warp's kStages x (16 K + 16 V) fp32 scales; per-block
+  // mode: kStages x (K, V)
   const uint32_t sbase = smem_base + kWarps * Geo::kWarpBytes + warp * Geo::kScaleWarpBytes;
   float* const sptr = reinterpret_cast<float*>(wptr + (kWarps - warp) * Geo::kWarpBytes +
                                                warp * Geo::kScaleWarpBytes);
@@ -283,7 +287,21 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
   };
   load_page();
   const uint64_t kv_policy = l2_evict_first_policy();  // K/V is read once
+  // Per-block scales: lane 0 starts the two loads when it issues a tile and
+  // stores them beside the stage at its next issue, a whole tile later, so the
+  // loads' latency is hidden without a wait and without registers per stage.
+  float pend_k = 0.f, pend_v = 0.f;
+  int pend_stage = -1;
+  auto store_pending = [&]() {
+    if constexpr (kScl == kSclBlock) {
+      if (lane == 0 && pend_stage >= 0) {
+        *reinterpret_cast<float2*>(sptr + 2 * pend_stage) = make_float2(pend_k, pend_v);
+        pend_stage = -1;
+      }
+    }
+  };
   auto issue = [&](int stage) {
+    store_pending();
     if (lane == 0) {
       const int tok0 = pc.tile * kTile;
       int page = next_page;
@@ -292,6 +310,12 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
         page = -1;  // the TMA box lands outside the tensor and reads zeros
       }
       const int row = (page * a.Hkv + pc.kvh) * a.P + tok0 % a.P;
+      if constexpr (kScl == kSclBlock) {
+        const int64_t si = (int64_t)page * a.Hkv + pc.kvh;
+        pend_k = page >= 0 ? __ldg(a.k_scales + si) : 0.f;  // a page outside the pool: zeros, as its codes
+        pend_v = page >= 0 ? __ldg(a.v_scales + si) : 0.f;
+        pend_stage = stage;
+      }
       const uint32_t dst = wbase + stage * Geo::kStageBytes;
       const uint32_t bar = bar0 + 8 * stage;
       uint32_t tx = Geo::kStageBytes;
@@ -329,6 +353,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
 #pragma unroll
   for (int s = 0; s < kStages; ++s)
     if (f_issue < f_end) issue(s);
+  store_pending();
+  if constexpr (kScl == kSclBlock) __syncwarp();  // the first stages' scales are visible
 
   // --- consumer state
   Cursor cc;
@@ -347,7 +373,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
 #pragma unroll
   for (int j = 0; j < NT; ++j) qinv[j][0] = qinv[j][1] = 1.f;
   float unit_vs = 1.f;       // unit mode: the unit's V scale
-  float vref = 0.f, vinv = 0.f;  // token mode: largest V scale of the unit so far, 1 / it
+  float vref = 0.f, vinv = 0.f;  // token and block modes: largest V scale of the unit so far, 1 / it
 
   auto flush = [&](int64_t f_stop) {
     // f_stop: first flattened tile after this segment; cc is on its last tile
@@ -362,7 +388,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
     const int nchunks = (int)((a.unit_start[b + 1] - a.unit_start[b]) / a.Hkv);
     const bool final = (nchunks == 1) && seg_begin == s_u && f_stop == e_u;
     // factor from accumulator units to dequantised V units
-    const float vmul = kScl == kSclUnit ? unit_vs : (kScl == kSclToken ? vref : 1.f);
+    const float vmul = kScl == kSclUnit ? unit_vs : (kScl == kSclToken || kScl == kSclBlock ? vref : 1.f);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -441,7 +467,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
       sc = __ldg(a.k_scales + si) * a.logit_scale;
       unit_vs = __ldg(a.v_scales + si);
     }
-    if constexpr (kScl == kSclToken) {
+    if constexpr (kScl == kSclToken || kScl == kSclBlock) {
       vref = 0.f;
       vinv = 0.f;
     }
@@ -624,12 +650,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
                    qf[j][2 * kk + 1][1]);
         }
       }
+      // undo the Q scale (a power of two: exact); a tile lies in one page, so
+      // the block's K scale rides along
+      float tile_ks = 1.f;
+      if constexpr (kScl == kSclBlock) tile_ks = sptr[2 * stage];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {  // undo the Q scale (a power of two: exact)
-        s[j][0] *= qinv[j][0];
-        s[j][1] *= qinv[j][1];
-        s[j][2] *= qinv[j][0];
-        s[j][3] *= qinv[j][1];
+      for (int j = 0; j < NT; ++j) {
+        const float f0 = kScl == kSclBlock ? qinv[j][0] * tile_ks : qinv[j][0];
+        const float f1 = kScl == kSclBlock ? qinv[j][1] * tile_ks : qinv[j][1];
+        s[j][0] *= f0;
+        s[j][1] *= f1;
+        s[j][2] *= f0;
+        s[j][3] *= f1;
       }
     }
 
@@ -693,17 +725,20 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
         rthr[j][1] = (mn1 + kRescaleLog2) / sc;
       }
     }
-    // per-token V scales enter as weights on p relative to vref, the largest V
+    // per-token and per-block V scales enter as weights on p relative to vref, the largest V
     // scale of the unit so far, so that p * weight <= p stays in f16 range;
     // when vref grows the accumulator is rescaled like the running maximum
     float w0 = 1.f, w8 = 1.f;
-    if constexpr (kScl == kSclToken) {
-      // the largest V scale of the tile: with one or two heads per KV head the
+    if constexpr (kScl == kSclToken || kScl == kSclBlock) {
+      // the largest V scale of the tile; per block it is the tile's only one.
+      // Per token, with one or two heads per KV head the
       // tile's work is too short to hide a shuffle chain, so every thread
       // reads the tile's 16 V scales from the stage; with more heads the
       // chain is hidden and costs fewer instructions
       float vm;
-      if (a.G <= 2) {
+      if constexpr (kScl == kSclBlock) {
+        vm = vs0 = vs8 = sptr[2 * stage + 1];
+      } else if (a.G <= 2) {
         const float4* vp = reinterpret_cast<const float4*>(sptr + stage * (kScaleStageBytes / 4) + 16);
         float4 q4[4] = {vp[0], vp[1], vp[2], vp[3]};
         if (partial) {
@@ -751,7 +786,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
       float p3 = fast_exp2(fmaf(s[j][3], sc, -mref[j][1]));
       l[j][0] += p0 + p2;
       l[j][1] += p1 + p3;
-      if constexpr (kScl == kSclToken) {
+      if constexpr (kScl == kSclToken || kScl == kSclBlock) {
         p0 *= w0;
         p1 *= w0;
         p2 *= w8;
@@ -821,6 +856,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
     if (f_issue < f_end) {
       if (lane == 0) fence_proxy_async_smem();
       issue(stage);
+    } else {
+      store_pending();
     }
     if (++stage == kStages) {
       stage = 0;
@@ -1224,7 +1261,7 @@ namespace pfkv {
 namespace {
 
 // The decode entry for every scale mode: kSclHost takes k_scale / v_scale;
-// kSclUnit and kSclToken read the device arrays k_scales / v_scales (unit
+// kSclUnit, kSclToken and kSclBlock read the device arrays k_scales / v_scales (unit
 // mode: one scale per KV head when head_stride is 1, one for all when 0).
 int decode_entry(void* out, const void* q, const void* k_cache, const void* v_cache,
                  pfkv_cache_dtype cache_dtype, const int32_t* block_tables, int max_pages_per_seq,
@@ -1341,6 +1378,9 @@ int decode_entry(void* out, const void* q, const void* k_cache, const void* v_ca
   if (scl == kSclToken)
     return G <= 8 ? launch_decode<false, 1, kSclToken>(tmK, tmV, a, s)
                   : launch_decode<false, 2, kSclToken>(tmK, tmV, a, s);
+  if (scl == kSclBlock)
+    return G <= 8 ? launch_decode<false, 1, kSclBlock>(tmK, tmV, a, s)
+                  : launch_decode<false, 2, kSclBlock>(tmK, tmV, a, s);
   return G <= 8 ? launch_decode<false, 1, kSclHost>(tmK, tmV, a, s)
                 : launch_decode<false, 2, kSclHost>(tmK, tmV, a, s);
 }
@@ -1377,6 +1417,7 @@ int pfkv_paged_decode_attn_scaled(void* out, const void* q, const void* k_cache,
     case PFKV_SCALE_TENSOR: scl = kSclUnit; break;
     case PFKV_SCALE_HEAD: scl = kSclUnit; stride = 1; break;
     case PFKV_SCALE_TOKEN: scl = kSclToken; break;
+    case PFKV_SCALE_BLOCK: scl = kSclBlock; break;
     default:
       clear_error();
       return fail(PFKV_ERR_INVALID_ARG, "paged_decode_scaled: unknown granularity %d", (int)granularity);

@@ -1,0 +1,470 @@
+// sparse_decode.cu -- one decode step's attention over a list of pages per
+// (request, KV head) of the paged e4m3 cache.
+//
+// For request b, KV head h and its list of logical pages, with T the tokens
+// t < L_b of the listed pages:
+//   s_t = softmax_scale * sum_d q[d] * val(K_t[d]) * ks(t),
+//   out = sum_{t in T} e^{s_t - m} val(V_t) vs(t) / sum_{t in T} e^{s_t - m},
+// with the scales of the tensor, the KV head, or the page.
+//
+// One cluster of up to 8 CTAs per (request, KV head), four warps a CTA.  Each
+// warp takes a contiguous run of the list's 16-token tiles: its lanes look up 32
+// pages at a time (list, block table, scales: one chain of loads for all of
+// them), and a ring of TMA stages keeps its K and V tiles in flight.  The warps'
+// states (m, l, o) stay in shared memory and are joined by log-sum-exp through
+// distributed shared memory, so the whole step is one launch without scratch in
+// global memory.  Long lists are bounded by HBM; short ones by the chain
+// length -> list -> block table -> first tile -> join.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "pfkv_internal.h"
+#include "pfkv_ptx.cuh"
+#include "pfkv_tc.cuh"
+#include "pfkv_tile.cuh"
+
+namespace pfkv {
+namespace {
+
+constexpr int kD = 128;
+constexpr int kTile = tile::kTokens;
+constexpr int kWarps = 4;
+constexpr int kStages = 3;
+constexpr int kMaxCluster = 8;
+constexpr int kStageBytes = 2 * tile::kSlabBytes;       // K, then V
+constexpr int kWarpBytes = kStages * kStageBytes;       // also holds the warp's final state
+constexpr int kSmemBytes = kWarps * kWarpBytes + 1024;  // + alignment slack
+constexpr int kMaxG = 16;
+static_assert(kMaxG * (kD + 2) * 4 <= kWarpBytes, "a warp's state fits its ring");
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+// A head's reference maximum is only raised when a score exceeds it by more
+// than this (log2 units), so p stays at most 2^8: exact enough in f16 and f32.
+constexpr float kRescaleLog2 = 8.f;
+
+struct SparseArgs {
+  uint16_t* out;
+  const uint16_t* q;
+  const float* k_scales;
+  const float* v_scales;
+  const int32_t* selected;  // [B][Hkv][K]
+  const int32_t* block_tables;
+  const int32_t* context_lens;
+  float* lse;
+  int32_t* status;  // [B][Hkv] or null
+  int Hq, Hkv, G, P, max_pages, K;
+  int64_t num_pages;
+  int page_stride, head_stride;  // scale index = page * page_stride + head * head_stride
+  float logit_scale;             // softmax_scale * log2(e)
+};
+
+template <int NT>
+__global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
+    sparse_decode_kernel(const __grid_constant__ CUtensorMap tmK, const __grid_constant__ CUtensorMap tmV,
+                         const SparseArgs a) {
+  extern __shared__ uint8_t smem_raw[];
+  __shared__ __align__(8) uint64_t bars[kWarps][kStages];
+  __shared__ float4 meta[kWarps][kStages];  // of the stage's tile: K scale, V scale, valid tokens
+  __shared__ uint32_t err;
+
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int g = lane >> 2, t = lane & 3;
+  const int nc = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
+  const int64_t unit = blockIdx.x / nc;
+  const int b = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
+  const uint32_t smem_base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+  const uint32_t wbase = smem_base + warp * kWarpBytes;
+  uint8_t* const wptr = smem_raw + (smem_base - smem_u32(smem_raw)) + warp * kWarpBytes;
+  const uint32_t bar0 = smem_u32(&bars[warp][0]);
+  if (threadIdx.x == 0) err = 0;
+  if (lane == 0) {
+#pragma unroll
+    for (int s = 0; s < kStages; ++s) mbar_init(bar0 + 8 * s, 1);
+    fence_mbar_init();
+    prefetch_tensormap(&tmK);
+    prefetch_tensormap(&tmV);
+  }
+  __syncthreads();
+
+  uint32_t bits = 0;
+  int L = a.context_lens[b];
+  const int cap = a.max_pages * a.P;
+  if (L < 0 || L > cap) {
+    bits |= kErrBadContext;
+    L = L < 0 ? 0 : cap;
+  }
+  const int npages = (L + a.P - 1) / a.P;
+  // listed pages are distinct, so no more than npages entries say anything
+  const int nslots = min(a.K, npages);
+  const int tpp = a.P / kTile;  // tiles per page
+  const int nw = nc * kWarps, gw = rank * kWarps + warp;
+  const int64_t F = (int64_t)nslots * tpp;
+  const int64_t f_end = (gw + 1) * F / nw;
+  int64_t f = gw * F / nw;  // next tile to issue
+
+  // ---------------- pages of list entries slot0 .. slot0 + 31, one per lane
+  int slot0 = 0, page = 0, tokens = 0;
+  float ks = 0.f, vs = 0.f;
+  auto look_up = [&](int s0) {
+    slot0 = s0;
+    tokens = 0;
+    const int slot = s0 + lane;
+    if ((int64_t)slot * tpp >= f_end) return;
+    const int logical = __ldg(a.selected + unit * a.K + slot);
+    if (logical < 0) return;  // padding
+    if (logical >= npages) {
+      bits |= kErrBadTopk;
+      return;
+    }
+    page = __ldg(a.block_tables + (int64_t)b * a.max_pages + logical);
+    if (page < 0 || (int64_t)page >= a.num_pages) {
+      bits |= kErrBadPage;
+      return;
+    }
+    const int64_t si = (int64_t)page * a.page_stride + h * a.head_stride;
+    ks = __ldg(a.k_scales + si);
+    vs = __ldg(a.v_scales + si);
+    tokens = min(a.P, L - logical * a.P);
+  };
+  if (f < f_end) look_up((int)(f / tpp));
+
+  // ---------------- producer: the next tile with tokens into `stage`
+  const uint64_t kv_policy = l2_evict_first_policy();
+  int slot = (int)(f / tpp), sub = (int)(f - (int64_t)slot * tpp);
+  int issued = 0;
+  auto issue = [&](int stage) {
+    while (f < f_end) {
+      if (slot - slot0 >= 32) look_up(slot);
+      const int src = slot - slot0;
+      const int valid = min(kTile, __shfl_sync(0xFFFFFFFFu, tokens, src) - sub * kTile);
+      const int pg = __shfl_sync(0xFFFFFFFFu, page, src);
+      const float k1 = __shfl_sync(0xFFFFFFFFu, ks, src), v1 = __shfl_sync(0xFFFFFFFFu, vs, src);
+      if (valid <= 0) {  // nothing (more) in this page
+        f += tpp - sub;
+        ++slot;
+        sub = 0;
+        continue;
+      }
+      if (lane == 0) {
+        const int row = (pg * a.Hkv + h) * a.P + sub * kTile;  // the cache has fewer than 2^31 rows
+        meta[warp][stage] = make_float4(k1, v1, __int_as_float(valid), 0.f);
+        const uint32_t bar = bar0 + 8 * stage, dst = wbase + stage * kStageBytes;
+        mbar_arrive_expect_tx(bar, kStageBytes);
+        tma_load_2d_hint(dst, &tmK, 0, row, bar, kv_policy);
+        tma_load_2d_hint(dst + tile::kSlabBytes, &tmV, 0, row, bar, kv_policy);
+      }
+      ++issued;
+      ++f;
+      if (++sub == tpp) {
+        sub = 0;
+        ++slot;
+      }
+      break;
+    }
+  };
+#pragma unroll
+  for (int s = 0; s < kStages; ++s) issue(s);
+
+  // ---------------- consumer
+  uint32_t qf[NT][8][2];
+  float qinv[NT][2], mref[NT][2], rthr[NT][2], l[NT][2], o[NT][8][4];
+  tile::load_q<NT>(a.q + ((int64_t)b * a.Hq + (int64_t)h * a.G) * kD, a.G, lane, qf, qinv);
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    mref[j][0] = mref[j][1] = rthr[j][0] = rthr[j][1] = -INFINITY;
+    l[j][0] = l[j][1] = 0.f;
+#pragma unroll
+    for (int i = 0; i < 8; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
+  }
+  // V scales enter as weights on p relative to vref, the largest so far, so that
+  // p keeps f16's range; o is rescaled when vref grows
+  float vref = 0.f, vinv = 0.f;
+  const float sc = a.logit_scale;
+  int stage = 0, done = 0;
+  uint32_t phase = 0;
+  bool timed_out = false;
+  while (done < issued) {
+    if (!mbar_wait(bar0 + 8 * stage, phase)) {
+      timed_out = true;
+      break;
+    }
+    const float4 mt = meta[warp][stage];
+    const int n = __float_as_int(mt.z);
+    const uint8_t* kb = wptr + stage * kStageBytes;
+    float s[NT][4];
+    tile::scores<NT>(kb, lane, qf, s);
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float f0 = qinv[j][0] * mt.x, f1 = qinv[j][1] * mt.x;
+      s[j][0] *= f0;
+      s[j][1] *= f1;
+      s[j][2] *= f0;
+      s[j][3] *= f1;
+      if (n < kTile) {
+        if (g >= n) s[j][0] = s[j][1] = -INFINITY;
+        if (g + 8 >= n) s[j][2] = s[j][3] = -INFINITY;
+      }
+    }
+    bool grow = false;
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      grow |= (fmaxf(s[j][0], s[j][2]) > rthr[j][0]) | (fmaxf(s[j][1], s[j][3]) > rthr[j][1]);
+    if (__any_sync(0xFFFFFFFFu, grow)) {
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        float mx0 = fmaxf(s[j][0], s[j][2]), mx1 = fmaxf(s[j][1], s[j][3]);
+#pragma unroll
+        for (int off = 4; off < 32; off <<= 1) {
+          mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
+          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
+        }
+        const float m0 = fmaxf(mref[j][0], mx0 * sc), m1 = fmaxf(mref[j][1], mx1 * sc);
+        const float a0 = fast_exp2(mref[j][0] - m0), a1 = fast_exp2(mref[j][1] - m1);
+        l[j][0] *= a0;
+        l[j][1] *= a1;
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[j][i][0] *= a0;
+          o[j][i][1] *= a1;
+          o[j][i][2] *= a0;
+          o[j][i][3] *= a1;
+        }
+        mref[j][0] = m0;
+        mref[j][1] = m1;
+        rthr[j][0] = (m0 + kRescaleLog2) / sc;
+        rthr[j][1] = (m1 + kRescaleLog2) / sc;
+      }
+    }
+    if (mt.y > vref) {  // warp-uniform
+      const float r = vref / mt.y;
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+          o[j][i][0] *= r;
+          o[j][i][1] *= r;
+          o[j][i][2] *= r;
+          o[j][i][3] *= r;
+        }
+      vref = mt.y;
+      vinv = 1.f / mt.y;
+    }
+    const float w = mt.y * vinv;
+    uint32_t pb[NT][2];
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const float p0 = fast_exp2(fmaf(s[j][0], sc, -mref[j][0])), p1 = fast_exp2(fmaf(s[j][1], sc, -mref[j][1]));
+      const float p2 = fast_exp2(fmaf(s[j][2], sc, -mref[j][0])), p3 = fast_exp2(fmaf(s[j][3], sc, -mref[j][1]));
+      l[j][0] += p0 + p2;
+      l[j][1] += p1 + p3;
+      pb[j][0] = movmatrix_trans(pack_f16x2(p0 * w, p1 * w));
+      pb[j][1] = movmatrix_trans(pack_f16x2(p2 * w, p3 * w));
+    }
+    tile::accumulate<NT>(kb + tile::kSlabBytes, lane, n, pb, o);
+    __syncwarp();
+    if (f < f_end) {
+      if (lane == 0) fence_proxy_async_smem();
+      issue(stage);
+    }
+    ++done;
+    if (++stage == kStages) {
+      stage = 0;
+      phase ^= 1u;
+    }
+  }
+  if (timed_out) {
+    bits |= kErrWaitTimeout;
+    for (; done < issued; ++done) {  // copies in flight land before the ring is used again
+      (void)mbar_wait(bar0 + 8 * stage, phase);
+      if (++stage == kStages) {
+        stage = 0;
+        phase ^= 1u;
+      }
+    }
+  }
+  bits = __reduce_or_sync(0xFFFFFFFFu, bits);
+  if (lane == 0 && bits) atomicOr(&err, bits);
+
+  // ---------------- the warp's state into its ring: o [G][128], then (m, l) [G]
+  __syncwarp();
+  float* const st = reinterpret_cast<float*>(wptr);
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float v = l[j][e];
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 4);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 8);
+      v += __shfl_xor_sync(0xFFFFFFFFu, v, 16);
+      const int head = 8 * j + 2 * t + e;
+      if (head < a.G) {
+        float4* d = reinterpret_cast<float4*>(st + head * kD + 16 * g);
+#pragma unroll
+        for (int k = 0; k < 4; ++k)
+          d[k] = make_float4(o[j][2 * k][e] * vref, o[j][2 * k][2 + e] * vref, o[j][2 * k + 1][e] * vref,
+                             o[j][2 * k + 1][2 + e] * vref);
+        if (g == 0) {
+          st[a.G * kD + 2 * head] = mref[j][e];
+          st[a.G * kD + 2 * head + 1] = v;
+        }
+      }
+    }
+  __syncwarp();
+  tc::cluster_sync();
+
+  // ---------------- join: a warp per head over the cluster's nw <= 32 states
+  for (int head = rank + nc * warp; head < a.G; head += nc * kWarps) {
+    float m = -INFINITY, den = 0.f;
+    if (lane < nw) {
+      const uint32_t at = tc::mapa(smem_base + (lane % kWarps) * kWarpBytes + (a.G * kD + 2 * head) * 4, lane / kWarps);
+      m = tc::ld_cluster_f32(at);
+      den = tc::ld_cluster_f32(at + 4);
+    }
+    float M = m;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xFFFFFFFFu, M, off));
+    const float w = m == -INFINITY ? 0.f : fast_exp2(m - M);
+    den *= w;
+#pragma unroll
+    for (int off = 16; off > 0; off >>= 1) den += __shfl_xor_sync(0xFFFFFFFFu, den, off);
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    for (int k = 0; k < nw; ++k) {
+      const float wk = __shfl_sync(0xFFFFFFFFu, w, k);
+      const float4 v = tc::ld_cluster_f32x4(
+          tc::mapa(smem_base + (k % kWarps) * kWarpBytes + (head * kD + 4 * lane) * 4, k / kWarps));
+      acc.x = fmaf(wk, v.x, acc.x);
+      acc.y = fmaf(wk, v.y, acc.y);
+      acc.z = fmaf(wk, v.z, acc.z);
+      acc.w = fmaf(wk, v.w, acc.w);
+    }
+    const float inv = den > 0.f ? 1.f / den : 0.f;  // nothing attended: zeros
+    const int64_t row = (int64_t)b * a.Hq + (int64_t)h * a.G + head;
+    reinterpret_cast<uint2*>(a.out + row * kD)[lane] =
+        make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (a.lse && lane == 0) a.lse[row] = den > 0.f ? (M + __log2f(den)) * kLn2 : -INFINITY;
+  }
+  if (a.status && rank == 0 && threadIdx.x == 0) {
+    uint32_t all = 0;
+    for (int r = 0; r < nc; ++r) all |= tc::ld_cluster_u32(tc::mapa(smem_u32(&err), r));
+    a.status[unit] = (int32_t)all;
+  }
+  __syncwarp();
+  tc::cluster_sync();  // no CTA leaves while another may still read its shared memory
+}
+
+// CTAs per (request, KV head): enough for the four resident CTAs of every SM,
+// as long as a warp keeps at least four tiles.
+int cluster_size(int64_t units, int64_t tiles, int sms) {
+  int c = 1;
+  while (c < kMaxCluster && units * c * 2 <= 4 * (int64_t)sms && tiles / (2 * c * kWarps) >= 4) c *= 2;
+  return c;
+}
+
+template <int NT>
+int launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const SparseArgs& a, int64_t units, cudaStream_t stream) {
+  auto kern = sparse_decode_kernel<NT>;
+  static std::atomic<uint64_t> smem_set{0};
+  const int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(kern), kSmemBytes, smem_set,
+                                      "paged_sparse_decode set smem attribute");
+  if (rc != PFKV_OK) return rc;
+  const int c = cluster_size(units, (int64_t)a.K * (a.P / kTile), device_sm_count());
+  cudaLaunchAttribute attr[1];
+  attr[0].id = cudaLaunchAttributeClusterDimension;
+  attr[0].val.clusterDim.x = (unsigned)c;
+  attr[0].val.clusterDim.y = 1;
+  attr[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3((unsigned)(units * c));
+  cfg.blockDim = dim3(kWarps * 32);
+  cfg.dynamicSmemBytes = kSmemBytes;
+  cfg.stream = stream;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (cudaLaunchKernelEx(&cfg, kern, tmK, tmV, a) != cudaSuccess) return check_cuda("paged_sparse_decode launch");
+  return check_cuda("paged_sparse_decode launch");
+}
+
+}  // namespace
+}  // namespace pfkv
+
+extern "C" int pfkv_paged_sparse_decode_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
+                                             pfkv_scale_granularity granularity, const float* k_scales,
+                                             const float* v_scales, const int32_t* selected, int top_pages,
+                                             const int32_t* block_tables, int max_pages_per_seq,
+                                             const int32_t* context_lens, int batch, int num_q_heads,
+                                             int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                             float softmax_scale, float* lse_out, int32_t* unit_status,
+                                             pfkv_stream_t stream) {
+  using namespace pfkv;
+  clear_error();
+  if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || num_pages <= 0 ||
+      max_pages_per_seq <= 0 || top_pages <= 0)
+    return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: bad sizes");
+  if (num_q_heads % num_kv_heads != 0)
+    return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: num_q_heads %% num_kv_heads != 0");
+  const int G = num_q_heads / num_kv_heads;
+  if (G > kMaxG) return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: group size %d > 16", G);
+  if (head_dim != kD) return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: head_dim %d != 128", head_dim);
+  if (page_size % kTile != 0)
+    return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: page_size %d not a multiple of 16", page_size);
+  int page_stride = 0, head_stride = 0;
+  switch (granularity) {
+    case PFKV_SCALE_TENSOR: break;
+    case PFKV_SCALE_HEAD: head_stride = 1; break;
+    case PFKV_SCALE_BLOCK:
+      page_stride = num_kv_heads;
+      head_stride = 1;
+      break;
+    case PFKV_SCALE_TOKEN:
+      return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: scales per token are not supported");
+    default:
+      return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: unknown granularity %d", (int)granularity);
+  }
+  if ((int64_t)num_pages * num_kv_heads * page_size >= (int64_t)1 << 31)
+    return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: cache has 2^31 or more token rows");
+  if ((int64_t)max_pages_per_seq * page_size >= (int64_t)1 << 30)
+    return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: block table too long");
+  if (!(softmax_scale > 0.f) || !isfinite(softmax_scale))
+    return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: softmax_scale must be finite and > 0");
+  const int64_t units = (int64_t)batch * num_kv_heads;
+  if (units > 0x7FFFFFFF / kMaxCluster) return fail(PFKV_ERR_UNSUPPORTED, "paged_sparse_decode: batch too large");
+  if (batch == 0) return PFKV_OK;
+  if (!out || !q || !k_cache || !v_cache || !k_scales || !v_scales || !selected || !block_tables || !context_lens)
+    return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: null pointer");
+  if (!aligned(out, 16) || !aligned(q, 16) || !aligned(k_cache, 16) || !aligned(v_cache, 16) ||
+      !aligned(k_scales, 4) || !aligned(v_scales, 4) || !aligned(selected, 4) || !aligned(block_tables, 4) ||
+      !aligned(context_lens, 4) || (lse_out && !aligned(lse_out, 4)) || (unit_status && !aligned(unit_status, 4)))
+    return fail(PFKV_ERR_INVALID_ARG, "paged_sparse_decode: misaligned pointer");
+  SparseArgs a;
+  a.out = static_cast<uint16_t*>(out);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.selected = selected;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.lse = lse_out;
+  a.status = unit_status;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.G = G;
+  a.P = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.K = top_pages;
+  a.num_pages = num_pages;
+  a.page_stride = page_stride;
+  a.head_stride = head_stride;
+  a.logit_scale = softmax_scale * kLog2e;
+  const cuuint64_t dims[2] = {kD, (cuuint64_t)num_pages * num_kv_heads * page_size};
+  const cuuint64_t strides[1] = {kD};
+  const cuuint32_t box[2] = {kD, (cuuint32_t)kTile};
+  CUtensorMap tmK, tmV;
+  int rc = encode_tensor_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(k_cache), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc == PFKV_OK)
+    rc = encode_tensor_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(v_cache), dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != PFKV_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  return G <= 8 ? launch<1>(tmK, tmV, a, units, s) : launch<2>(tmK, tmV, a, units, s);
+}

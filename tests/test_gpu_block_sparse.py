@@ -1,0 +1,374 @@
+"""Block-sparse decode on the GPU: key bounds and page lists equal to 64-bit
+numpy, attention over lists within the bound derived in
+block_reference.tolerance, and the calls of a decode step in a row."""
+import numpy as np
+import pytest
+
+import block_reference as ref
+from gpu_helpers import pf
+from guard_helpers import Guarded
+from test_gpu_block_scales import State, bf16, check_rows, context, dev, filled, tables
+
+pytestmark = pytest.mark.gpu
+
+
+# ------------------------------------------------------------------ bounds
+@pytest.mark.parametrize("H,P", [(2, 16), (1, 1), (3, 7), (48, 32), (1, 128)])
+def test_bounds_of_contexts_and_of_last_pages(H, P):
+    import torch
+    p, rng = pf(), np.random.default_rng(P)
+    lens = np.array([1, P, P + 1, 5 * P - 1, 0, 77], np.int32)
+    bt, pages = tables(rng, lens, P)
+    k = rng.integers(0, 256, (pages, H, P, 128)).astype(np.uint8)
+    k[(k & 127) == 127] = 0x22
+    k[rng.random((pages, H, P)) < 0.1] = 0
+    k[bt[2, 0]] = 0x80  # a page of -0
+    k[bt[3, 0], :, P // 2:] = 0x81  # rows of the smallest negative value
+    for b, m in enumerate(lens):
+        if m % P:
+            k[bt[b, m // P], :, m % P:] = 0x7E  # 448 past the context
+    got, sc = Guarded((pages, H, 2, 128), torch.int8, "cuda"), Guarded((pages, H), torch.float32, "cuda")
+    want, want_s = got.t.cpu().numpy().copy(), sc.t.cpu().numpy().copy()
+    for new in (lens, np.minimum(lens, 1), np.minimum(lens, P + 1)):
+        start = np.concatenate([[0], np.cumsum(new)]).astype(np.int32)
+        got.t.fill_(-91)
+        want[:] = -91
+        p.page_key_bounds(got.t, sc.t, dev(k), dev(bt), dev(lens), dev(start), int(new.max()))
+        torch.cuda.synchronize()
+        ref.bounds(k, want, want_s, bt, lens, start, int(new.max()))
+        got.check()
+        sc.check()
+        assert np.array_equal(got.t.cpu().numpy(), want)
+        assert np.array_equal(sc.t.cpu().numpy().view(np.uint32), want_s.view(np.uint32))
+
+
+def test_bounds_pass_over_nan_codes_and_what_does_not_fit():
+    import torch
+    p, rng, P = pf(), np.random.default_rng(4), 16
+    lens = np.array([40, 40, 40, 40], np.int32)
+    bt, pages = tables(rng, lens, P)
+    k = rng.integers(0, 0x70, (pages, 2, P, 128)).astype(np.uint8)
+    k[bt[0, 0], 0, 3, 7] = 0x7F
+    k[bt[0, 1], 1, 5:9, :] = 0xFF
+    bad = bt.copy()
+    bad[1, 1], bad[2, 0] = -1, pages
+    got = torch.full((pages, 2, 2, 128), -91, dtype=torch.int8, device="cuda")
+    sc = torch.full((pages, 2), -1.0, device="cuda")
+    want, want_s = got.cpu().numpy().copy(), sc.cpu().numpy().copy()
+    arg = np.array([40, 40, 40, 49], np.int32)  # the last is longer than its table
+    start = np.array([0, 40, 80, 120, 160], np.int32)
+    p.page_key_bounds(got, sc, dev(k), dev(bad), dev(arg), dev(start), 40)
+    torch.cuda.synchronize()
+    ref.bounds(k, want, want_s, bad, arg, start, 40)
+    assert np.array_equal(got.cpu().numpy(), want) and np.array_equal(sc.cpu().numpy(), want_s)
+
+
+# ------------------------------------------------------------------ select
+def random_bounds(rng, pages, H, flat=False):
+    lo = rng.integers(-127, 100, (pages, H, 1, 128))
+    hi = np.minimum(lo + rng.integers(0, 90, lo.shape), 127)
+    b = np.concatenate([lo, hi], 2).astype(np.int8)
+    if flat:
+        b[:] = b[:1, :1]
+    return b, np.exp2(rng.integers(-1, 1 if flat else 3, (pages, H)) * (0 if flat else 1)).astype(np.float32)
+
+
+def run_select(lens, Hq, Hkv, P, top, sink, recent, seed=0, flat=False, ks=False, width=None, qscale=1.0, qbits=None):
+    import torch
+    p, rng = pf(), np.random.default_rng(seed)
+    bt, pages = tables(rng, lens, P, width=width)
+    bnd, bs = random_bounds(rng, pages, Hkv, flat)
+    kscales = np.exp2(rng.integers(-9, -5, (pages, Hkv))).astype(np.float32) if ks else None
+    q, qv = bf16(rng.standard_normal((len(lens), Hq, 128)) * qscale)
+    if qbits is not None:
+        q, qv = bf16(np.broadcast_to(qbits, qv.shape))
+    sel = Guarded((len(lens), Hkv, top), torch.int32, "cuda")
+    st = Guarded((len(lens), Hkv), torch.int32, "cuda")
+    p.select_pages(sel.t, q, dev(bnd), dev(bs), dev(bt), dev(np.array(lens, np.int32)), P, sink, recent,
+                   k_scales=None if kscales is None else dev(kscales), unit_status=st.t)
+    torch.cuda.synchronize()
+    sel.check()
+    st.check()
+    assert int(st.t.abs().sum()) == 0
+    want = ref.select(qv, bnd, bs, kscales, bt, lens, P, top, sink, recent)
+    assert np.array_equal(sel.t.cpu().numpy(), want), (lens, top)
+
+
+@pytest.mark.parametrize("Hq,Hkv,P", [(8, 2, 16), (16, 1, 64), (4, 4, 48), (20, 4, 1), (7, 1, 128)])
+@pytest.mark.parametrize("top,sink,recent", [(1, 0, 0), (1, 0, 1), (5, 1, 2), (64, 64, 0), (33, 0, 3)])
+def test_select_equals_reference(Hq, Hkv, P, top, sink, recent):
+    lens = [0, 1, P * top, P * top + 1, 40 * P - P // 2, 700 * P]
+    run_select(lens, Hq, Hkv, P, top, sink, recent, seed=top, ks=top % 2 == 1)
+
+
+def test_select_ties_go_to_the_lower_page():
+    run_select([3000, 5001], 8, 2, 16, 100, 0, 0, flat=True)
+    run_select([50000], 8, 1, 16, 1000, 2, 3, flat=True)   # several CTAs a list
+    run_select([3000], 8, 2, 16, 17, 0, 1, qbits=np.zeros(128))  # every score is zero
+
+
+@pytest.mark.parametrize("top", [3, 255, 4097])
+def test_select_large_tables(top):
+    """Clusters of up to eight CTAs, shares of all sizes."""
+    run_select([16 * 5000, 16 * 4097, 17], 8, 1, 16, top, 1, 2, seed=1, ks=True)
+    run_select([8 * 30001], 3, 1, 8, top, 0, 0, seed=2)
+    run_select([4096 * 7] * 20, 8, 8, 16, min(top, 1700), 1, 1, seed=3)
+
+
+def test_select_table_much_wider_than_the_contexts():
+    run_select([16 * 100, 5, 16 * 77], 8, 2, 16, 20, 1, 1, width=393216)
+
+
+@pytest.mark.parametrize("qscale", [2.0 ** -133, 2.0 ** -100, 2.0 ** 120])
+def test_select_queries_of_any_size(qscale):
+    run_select([4000], 8, 1, 16, 40, 0, 0, qscale=qscale)
+
+
+def test_select_bad_pages_and_lengths():
+    import torch
+    p, rng, P, top = pf(), np.random.default_rng(9), 16, 4
+    lens = np.array([160, 160, 160], np.int32)
+    bt, pages = tables(rng, lens, P)
+    bnd, bs = random_bounds(rng, pages, 1)
+    q, qv = bf16(rng.standard_normal((3, 4, 128)))
+    bad = bt.copy()
+    bad[0, 3], bad[0, 6] = -2, pages
+    arg = np.array([160, -7, 161], np.int32)
+    sel = torch.empty((3, 1, top), dtype=torch.int32, device="cuda")
+    st = torch.empty((3, 1), dtype=torch.int32, device="cuda")
+    p.select_pages(sel, q, dev(bnd), dev(bs), dev(bad), dev(arg), P, 1, 1, unit_status=st)
+    torch.cuda.synchronize()
+    assert st.cpu().numpy().ravel().tolist() == [p.DEVERR["BAD_PAGE"], p.DEVERR["BAD_CONTEXT"], p.DEVERR["BAD_CONTEXT"]]
+    got = sel.cpu().numpy()
+    want = ref.select(qv, bnd, bs, None, bt, np.array([160, 0, 160]), P, top, 1, 1)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[2], want[2])
+    keep = [i for i in range(10) if i not in (3, 6)]
+    Q = ref.group_query(qv[0])
+    score = (bnd[bt[0], 0].astype(np.int64) * Q).sum((1, 2)) * bs[bt[0], 0].astype(np.float64)
+    score[[0, 9]] = np.inf
+    assert got[0, 0].tolist() == sorted(sorted(keep, key=lambda i: (-score[i], i))[:top])
+
+
+# ------------------------------------------------------------------ sparse
+def lists(rng, lens, Hkv, P, top, shuffled=False):
+    """Random distinct pages; some entries of padding, in front as well."""
+    sel = np.full((len(lens), Hkv, top), -1, np.int32)
+    for b, m in enumerate(lens):
+        n = -(-m // P)
+        for h in range(Hkv):
+            k = min(n, top) if (b + h) % 3 else int(rng.integers(0, min(n, top) + 1))
+            got = rng.choice(n, k, replace=False) if n else np.zeros(0, int)
+            if k and n - 1 not in got and h % 2:
+                got[0] = n - 1  # the last, partial page
+            width = min(n, top)
+            at = np.sort(rng.choice(width, k, replace=False)) if shuffled else np.arange(k)
+            sel[b, h, at] = got if shuffled else np.sort(got)
+    return sel
+
+
+def subset(c, bt_row, h, L, P, pages):
+    k, v, vs = context(c, bt_row, h, L, P)
+    t = np.concatenate([np.arange(i * P, min((i + 1) * P, L)) for i in pages] + [np.zeros(0, int)]).astype(int)
+    return k[t], v[t], vs[t]
+
+
+@pytest.mark.parametrize("Hq,Hkv,P,top,lens", [
+    (8, 2, 16, 4, (1, 16, 17, 300, 0)), (16, 1, 64, 40, (5000, 64, 63)), (4, 4, 48, 1, (33, 96, 500)),
+    (20, 4, 128, 9, (1000, 3, 129)), (64, 8, 16, 128, (2049, 257, 1, 31, 512, 6000)), (7, 1, 96, 33, (5000, 9000)),
+    (48, 48, 16, 20, (700,)), (8, 1, 16, 1000, (16000, 15999, 40))])
+@pytest.mark.parametrize("gran", [0, 1, 3])
+def test_sparse_decode_matches_reference(Hq, Hkv, P, top, lens, gran):
+    import torch
+    p, rng = pf(), np.random.default_rng(top + gran)
+    bt, c = filled(rng, list(lens), Hkv, P)
+    if gran != 3:
+        for x in "kv":
+            s = (rng.random(Hkv if gran else 1) * 0.01 + 0.002).astype(np.float32)
+            c[x + "dev"] = s
+            c[x + "s"] = np.broadcast_to(s, (c[x].shape[0], Hkv))
+    sel = lists(rng, lens, Hkv, P, top, shuffled=gran == 1)
+    q, qv = bf16(rng.standard_normal((len(lens), Hq, 128)))
+    out, lse = Guarded(q.shape, torch.bfloat16, "cuda"), Guarded(q.shape[:2], torch.float32, "cuda")
+    st = Guarded((len(lens), Hkv), torch.int32, "cuda")
+    p.paged_sparse_decode_attn(out.t, q, dev(c["k"]), dev(c["v"]), gran, dev(c.get("kdev", c["ks"])),
+                               dev(c.get("vdev", c["vs"])), dev(sel), dev(bt), dev(np.array(lens, np.int32)), 0.088,
+                               lse_out=lse.t, unit_status=st.t)
+    torch.cuda.synchronize()
+    for x in (out, lse, st):
+        x.check()
+    assert int(st.t.abs().sum()) == 0
+    sets = [[subset(c, bt[b], h, m, P, sel[b, h][sel[b, h] >= 0]) for h in range(Hkv)] for b, m in enumerate(lens)]
+    check_rows(out.t.float().cpu().numpy().astype(np.float64), lse.t.cpu().numpy(), qv, sets, 0.088, f"{lens} {top}")
+
+
+def test_sparse_over_all_pages_is_dense_decode():
+    import torch
+    p, rng, P = pf(), np.random.default_rng(6), 16
+    lens = [777, 1, 4096]
+    bt, c = filled(rng, lens, 2, P)
+    top = 256
+    sel = np.full((3, 2, top), -1, np.int32)
+    for b, m in enumerate(lens):
+        sel[b, :, :-(-m // P)] = np.arange(-(-m // P))
+    q, qv = bf16(rng.standard_normal((3, 8, 128)))
+    args = [dev(c["k"]), dev(c["v"]), p.SCALE_BLOCK, dev(c["ks"]), dev(c["vs"])]
+    ld = dev(np.array(lens, np.int32))
+    for sparse in (False, True):
+        out, lse = torch.empty_like(q), torch.empty((3, 8), device="cuda")
+        if sparse:
+            p.paged_sparse_decode_attn(out, q, *args, dev(sel), dev(bt), ld, 0.088, lse_out=lse)
+        else:
+            p.paged_decode_attn_scaled(out, q, *args, dev(bt), ld, 0.088, lse_out=lse)
+        sets = [[context(c, bt[b], h, m, P) for h in range(2)] for b, m in enumerate(lens)]
+        check_rows(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy(), qv, sets, 0.088, f"sparse {sparse}")
+
+
+def test_sparse_bad_entries_are_passed_over():
+    import torch
+    p, rng, P = pf(), np.random.default_rng(8), 16
+    lens = [100, 100, 100, 100]
+    bt, c = filled(rng, lens, 1, P)
+    bad = bt.copy()
+    bad[1, 2], bad[1, 3] = -1, 2 ** 31 - 1
+    sel = np.array([[0, 7, 2 ** 31 - 1, 3], [1, 2, 3, -1], [-5, -1, -1, -1], [6, 0, 1, 2]], np.int32)[:, None]
+    arg = np.array([100, 100, 100, 113], np.int32)  # the last is longer than its table: clamped to 112
+    q, qv = bf16(rng.standard_normal((4, 8, 128)))
+    out, lse = torch.empty_like(q), torch.empty((4, 8), device="cuda")
+    st = torch.empty((4, 1), dtype=torch.int32, device="cuda")
+    c["v"][bt[3, 6]] = c["v"][bt[0, 1]]  # no NaN codes in the rows that the clamped length reaches
+    c["k"][bt[3, 6]] = c["k"][bt[0, 1]]
+    p.paged_sparse_decode_attn(out, q, dev(c["k"]), dev(c["v"]), p.SCALE_BLOCK, dev(c["ks"]), dev(c["vs"]), dev(sel),
+                               dev(bad), dev(arg), 0.088, lse_out=lse, unit_status=st)
+    torch.cuda.synchronize()
+    E = p.DEVERR
+    assert st.cpu().numpy().ravel().tolist() == [E["BAD_TOPK"], E["BAD_PAGE"], 0, E["BAD_CONTEXT"]]
+    sets = [[subset(c, bt[0], 0, 100, P, [0, 3])], [subset(c, bt[1], 0, 100, P, [1])], [(np.zeros((0, 128)),) * 3],
+            [subset(c, bt[3], 0, 112, P, [6, 0, 1, 2])]]
+    check_rows(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy(), qv, sets, 0.088)
+
+
+@pytest.mark.parametrize("size", [2.0 ** -130, 2.0 ** 100])
+def test_sparse_queries_of_any_size(size):
+    import torch
+    p, rng, P = pf(), np.random.default_rng(12), 16
+    bt, c = filled(rng, [500], 2, P)
+    sel = np.broadcast_to(np.arange(0, 32, 2, dtype=np.int32), (1, 2, 16)).copy()
+    q, qv = bf16(rng.standard_normal((1, 8, 128)) * size)
+    scale = float(np.float32(0.088 / size)) if size > 1 else 0.088
+    out, lse = torch.empty_like(q), torch.empty((1, 8), device="cuda")
+    p.paged_sparse_decode_attn(out, q, dev(c["k"]), dev(c["v"]), p.SCALE_BLOCK, dev(c["ks"]), dev(c["vs"]), dev(sel),
+                               dev(bt), dev(np.array([500], np.int32)), scale, lse_out=lse)
+    sets = [[subset(c, bt[0], h, 500, P, sel[0, h]) for h in range(2)]]
+    check_rows(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy(), qv, sets, scale)
+
+
+# --------------------------------------------------------------- a decode step
+def test_steps_of_append_bounds_select_attend():
+    """Prompts, then decode steps with all the calls on one stream without a
+    wait between them, eager and replayed from a graph on another stream."""
+    import torch
+    p, P, H, Hq, top = pf(), 16, 2, 8, 6
+    lens = [150, 47, 300]
+    full = [m + 8 for m in lens]
+    st = State(31, full, H, 128, P)
+    bnd = torch.zeros((st.pages, H, 2, 128), dtype=torch.int8, device="cuda")
+    bs = torch.zeros((st.pages, H), device="cuda")
+    rb, rs = bnd.cpu().numpy().copy(), bs.cpu().numpy().copy()
+    bt = dev(st.bt)
+    ctx, start = dev(np.array(lens, np.int32)), dev(np.concatenate([[0], np.cumsum(lens)]).astype(np.int32))
+    sel = torch.empty((3, H, top), dtype=torch.int32, device="cuda")
+    q, qv = bf16(st.rng.standard_normal((3, Hq, 128)))
+    out, lse = torch.empty_like(q), torch.empty((3, Hq), device="cuda")
+    stat = torch.full((2, 3, H), -1, dtype=torch.int32, device="cuda")
+    scale = 2.0 ** -12
+    kn = {x: torch.zeros((3, H, 128), dtype=torch.bfloat16, device="cuda") for x in "kv"}
+
+    st.append(lens, lens)
+    p.page_key_bounds(bnd, bs, st.g["k"].t, bt, ctx, start, max(lens))
+    ref.bounds(st.ref["k"], rb, rs, st.bt, lens, start.cpu().numpy(), max(lens))
+    start.copy_(dev(np.arange(4, dtype=np.int32)))
+
+    def step():
+        p.kv_append_fp8_block(kn["k"], kn["v"], st.g["k"].t, st.g["v"].t, st.s["k"].t, st.s["v"].t, bt, ctx, start, 1)
+        p.page_key_bounds(bnd, bs, st.g["k"].t, bt, ctx, start, 1)
+        p.select_pages(sel, q, bnd, bs, bt, ctx, P, 1, 1, k_scales=st.s["k"].t, unit_status=stat[0])
+        p.paged_sparse_decode_attn(out, q, st.g["k"].t, st.g["v"].t, p.SCALE_BLOCK, st.s["k"].t, st.s["v"].t, sel, bt,
+                                   ctx, scale, lse_out=lse, unit_status=stat[1])
+
+    side = torch.cuda.Stream()
+    graph = None
+    for t in range(8):
+        now = [m + t + 1 for m in lens]
+        new = {}
+        for x in "kv":
+            r, rv = bf16(st.rng.standard_normal((3, H, 128)) * 2.0 ** (t - 3))
+            kn[x].copy_(r)
+            new[x] = rv
+        qt, qv = bf16(st.rng.standard_normal((3, Hq, 128)))
+        q.copy_(qt)
+        ctx.copy_(dev(np.array(now, np.int32)))
+        torch.cuda.synchronize()
+        if t < 3:
+            step()
+        else:
+            if graph is None:
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph):
+                    step()
+            with torch.cuda.stream(side):
+                graph.replay()
+        torch.cuda.synchronize()
+        for x in "kv":
+            ref.append(new[x], st.ref[x], st.ref[x + "s"], st.bt, now, [0, 1, 2, 3], 1)
+        st.check(f"step {t}")
+        ref.bounds(st.ref["k"], rb, rs, st.bt, now, [0, 1, 2, 3], 1)
+        assert np.array_equal(bnd.cpu().numpy(), rb) and np.array_equal(bs.cpu().numpy(), rs)
+        want = ref.select(qv, rb, rs, st.ref["ks"], st.bt, now, P, top, 1, 1)
+        assert np.array_equal(sel.cpu().numpy(), want)
+        assert int(stat.abs().sum()) == 0
+        c = {"k": st.ref["k"], "v": st.ref["v"], "ks": st.ref["ks"], "vs": st.ref["vs"]}
+        sets = [[subset(c, st.bt[b], h, m, P, want[b, h][want[b, h] >= 0]) for h in range(H)] for b, m in enumerate(now)]
+        check_rows(out.float().cpu().numpy().astype(np.float64), lse.cpu().numpy(), qv, sets, scale, f"step {t}")
+
+
+def test_refusals_of_tensors_that_do_not_match():
+    import torch
+    p = pf()
+    z = lambda *s, dt=torch.float32: torch.zeros(s, dtype=dt, device="cuda")
+    q, bnd, bs = z(2, 8, 128, dt=torch.bfloat16), z(9, 2, 2, 128, dt=torch.int8), z(9, 2)
+    bt, ctx, sel = z(2, 4, dt=torch.int32), z(2, dt=torch.int32), z(2, 2, 3, dt=torch.int32)
+    k, start = z(9, 2, 16, 128, dt=torch.uint8), z(3, dt=torch.int32)
+    good = dict(selected=sel, q=q, bounds=bnd, bound_scales=bs, block_tables=bt, context_lens=ctx, page_size=16)
+    p.select_pages(**good)
+    for name, t in (("selected", sel.long()), ("selected", sel[:, :1]), ("q", q.float()), ("bounds", bnd[:8]),
+                    ("bounds", bnd.view(torch.uint8)), ("context_lens", ctx[:1]), ("block_tables", bt[:1]),
+                    ("q", q.cpu()), ("k_scales", z(9)), ("unit_status", z(2, 3, dt=torch.int32)),
+                    ("q", z(2, 128, 8, dt=torch.bfloat16).transpose(1, 2))):
+        with pytest.raises(ValueError):
+            p.select_pages(**{**good, name: t})
+    with pytest.raises(p.PfkvError):
+        p.select_pages(**good, sink_pages=2, recent_pages=2)
+    good = dict(out=q.clone(), q=q, k_cache=k, v_cache=k, granularity=p.SCALE_BLOCK, k_scales=bs, v_scales=bs,
+                selected=sel, block_tables=bt, context_lens=ctx, softmax_scale=0.1)
+    p.paged_sparse_decode_attn(**good)
+    for name, t in (("granularity", p.SCALE_HEAD), ("granularity", p.SCALE_TENSOR), ("k_scales", bs.double()),
+                    ("v_cache", k[:8]), ("selected", sel[:, :1]), ("out", q.half()), ("lse_out", z(2, 7))):
+        with pytest.raises(ValueError):
+            p.paged_sparse_decode_attn(**{**good, name: t})
+    for name, t in (("granularity", p.SCALE_TOKEN), ("granularity", 9), ("softmax_scale", 0.0)):
+        with pytest.raises(p.PfkvError):
+            p.paged_sparse_decode_attn(**{**good, name: t})
+    x = z(5, 2, 128, dt=torch.bfloat16)
+    good = dict(k_new=x, v_new=x, k_cache=k, v_cache=k.clone(), k_scales=bs, v_scales=bs.clone(), block_tables=bt,
+                context_lens=ctx, new_start=start, max_new_len=1)
+    p.kv_append_fp8_block(**good)
+    for name, t in (("v_new", x[:4]), ("v_cache", None), ("k_cache", k.float()), ("new_start", start[:2]),
+                    ("k_scales", z(9, 1)), ("k_new", x.float())):
+        with pytest.raises(ValueError):
+            p.kv_append_fp8_block(**{**good, name: t})
+    good = dict(bounds=bnd, bound_scales=bs, k_cache=k, block_tables=bt, context_lens=ctx, new_start=start, max_new_len=1)
+    p.page_key_bounds(**good)
+    for name, t in (("bounds", z(9, 2, 128, dt=torch.int8)), ("bound_scales", z(9)), ("k_cache", k.float())):
+        with pytest.raises(ValueError):
+            p.page_key_bounds(**{**good, name: t})
+    torch.cuda.synchronize()
