@@ -331,7 +331,7 @@ PFKV_API int pfkv_paged_decode_attn_scaled(void *out, const void *q, const void 
  * page and the list is made by the library.  Three calls, in a decode step
  * after the append: pfkv_page_key_bounds brings the summaries of the pages the
  * step touched up to date, pfkv_select_pages lists pages, and
- * pfkv_paged_sparse_decode_attn attends to them.  None takes a workspace.
+ * pfkv_paged_sparse_decode_attn attends to them.
  *
  * unit_status (the last two calls): optional int32 [batch][num_kv_heads],
  * device; every entry is written, 0 or an OR of PFKV_DEVERR_* bits.
@@ -378,15 +378,21 @@ PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const voi
  *                 are common to all pages of a head
  * A page outside the pool scores lowest (PFKV_DEVERR_BAD_PAGE); a length
  * outside the table is clamped (PFKV_DEVERR_BAD_CONTEXT).
+ *   workspace     device scratch of at least pfkv_select_pages_workspace_size()
+ *                 bytes (query it on the device that will run the call),
+ *                 256-byte aligned; contents on entry are ignored.  It holds the
+ *                 scores, 4 bytes per KV head and block-table entry; 0 bytes and
+ *                 NULL where few short lists keep them on the SMs.
  * Supported: head_dim 128; G in 1..16; sink_pages + recent_pages <= top_pages;
- * max_pages_per_seq <= 393216; any page_size. */
+ * num_pages * num_kv_heads < 2^31; any page_size. */
+PFKV_API size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq);
 PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *bounds,
                                const float *bound_scales, const float *k_scales,
                                const int32_t *block_tables, int max_pages_per_seq,
                                const int32_t *context_lens, int batch, int num_q_heads, int num_kv_heads,
                                int head_dim, int page_size, int64_t num_pages, int top_pages,
-                               int sink_pages, int recent_pages, int32_t *unit_status,
-                               pfkv_stream_t stream);
+                               int sink_pages, int recent_pages, void *workspace,
+                               size_t workspace_bytes, int32_t *unit_status, pfkv_stream_t stream);
 
 /* paged_sparse_decode_attn -- paged_decode_attn_scaled over listed pages only:
  * for request b and KV head h the softmax runs over the tokens t < L_b of the

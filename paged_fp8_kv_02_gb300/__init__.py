@@ -19,7 +19,8 @@ from . import _build
 
 __all__ = [
     "PfkvError", "load", "lib_path", "kv_append_fp8", "kv_append_bf16",
-    "kv_append_fp8_scaled", "kv_append_fp8_block", "page_key_bounds", "select_pages", "paged_sparse_decode_attn",
+    "kv_append_fp8_scaled", "kv_append_fp8_block", "page_key_bounds", "select_pages_workspace_size", "select_pages",
+    "paged_sparse_decode_attn",
     "paged_decode_workspace_size", "paged_decode_attn", "paged_decode_attn_noalloc", "paged_decode_attn_scaled",
     "paged_prefill_workspace_size", "paged_prefill_attn",
     "SCALE_TENSOR", "SCALE_HEAD", "SCALE_TOKEN", "SCALE_BLOCK",
@@ -75,8 +76,9 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "pfkv_kv_append_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
                                                i32, i64, vp]),
             "pfkv_page_key_bounds": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, vp]),
+            "pfkv_select_pages_workspace_size": (sz, [i32, i32, i32]),
             "pfkv_select_pages": (i32, [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, i32,
-                                        i32, vp, vp]),
+                                        i32, vp, sz, vp, vp]),
             "pfkv_paged_sparse_decode_attn": (i32, [vp, vp, vp, vp, i32, vp, vp, vp, i32, vp, i32, vp, i32, i32,
                                                     i32, i32, i32, i64, f32, vp, vp, vp]),
             "pfkv_paged_decode_workspace_size": (sz, [i32, i32, i32, i32, i32, i64]),
@@ -123,13 +125,14 @@ def _ptr(t):
         raise ValueError("expected a CUDA tensor")
     if not t.is_contiguous():
         raise ValueError("expected a contiguous tensor")
-    return ctypes.c_void_p(t.data_ptr())
+    return t.data_ptr()
 
 
 def _stream(stream):
     import torch
-    s = torch.cuda.current_stream() if stream is None else stream
-    return ctypes.c_void_p(s.cuda_stream)
+    if stream is not None:
+        return stream.cuda_stream
+    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
 
 
 def _check(fn: str, rc: int):
@@ -186,29 +189,31 @@ def kv_append_fp8_scaled(k_new, v_new, k_cache, v_cache, slot_mapping, granulari
     _check("kv_append_fp8_scaled", rc)
 
 
-def _want(name: str, t, dtype, shape, device) -> int:
+def _want(name: str, t, dtype, shape, device: int) -> int:
     """Device address of a tensor that has to be just this; ValueError otherwise."""
-    if t.dtype is not dtype or t.shape != shape or t.device != device or not t.is_contiguous():
-        raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on {device}, got "
-                         f"{t.dtype} {tuple(t.shape)} on {t.device}")
-    return t.data_ptr()
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device and t.is_contiguous():
+        return t.data_ptr()
+    raise ValueError(f"{name}: expected a contiguous {dtype} tensor of shape {tuple(shape)} on the call's device "
+                     f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
-def _call(fn: str, device, stream, *args):
-    """One entry point on `device`: its current stream unless one is given."""
+def _call(fn: str, device: int, stream, *args):
+    """One entry point on a device: its current stream unless one is given."""
     import torch
-    if device.type != "cuda":
+    if device < 0:
         raise ValueError("expected CUDA tensors")
     if stream is None:
-        stream = torch.cuda.current_stream(device)
-    elif stream.device != device:
-        raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to {device}")
-    f = getattr(load(), "pfkv_" + fn)
-    if device.index == torch.cuda.current_device():
-        rc = f(*args, stream.cuda_stream)
+        handle = torch._C._cuda_getCurrentRawStream(device)
+    elif stream.device.index != device:
+        raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to device {device}")
+    else:
+        handle = stream.cuda_stream
+    f = getattr(_lib or load(), "pfkv_" + fn)
+    if device == torch._C._cuda_getDevice():
+        rc = f(*args, handle)
     else:
         with torch.cuda.device(device):
-            rc = f(*args, stream.cuda_stream)
+            rc = f(*args, handle)
     _check(fn, rc)
 
 
@@ -222,7 +227,7 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, bloc
     new tokens; new_start int32 [B+1]; max_new_len bounds every n_b.  For K
     alone pass v_new = v_cache = v_scales = None."""
     import torch
-    dev = k_new.device
+    dev = k_new.get_device()
     T, H, D = k_new.shape
     pages, _, P, _ = k_cache.shape
     B, maxp = block_tables.shape
@@ -250,7 +255,7 @@ def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, n
     [pages][H] times the page's K scale, from the e4m3 k_cache uint8
     [pages][H][P][128].  max_new_len bounds the counts."""
     import torch
-    dev = k_cache.device
+    dev = k_cache.get_device()
     pages, H, P, D = k_cache.shape
     B, maxp = block_tables.shape
     _call("page_key_bounds", dev, stream, _want("bounds", bounds, torch.int8, (pages, H, 2, D), dev),
@@ -261,27 +266,42 @@ def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, n
           _want("new_start", new_start, torch.int32, (B + 1,), dev), B, int(max_new_len), H, D, P, pages)
 
 
+def select_pages_workspace_size(batch: int, num_kv_heads: int, max_pages_per_seq: int) -> int:
+    return int(load().pfkv_select_pages_workspace_size(batch, num_kv_heads, max_pages_per_seq))
+
+
 def select_pages(selected, q, bounds, bound_scales, block_tables, context_lens, page_size: int, sink_pages: int = 1,
-                 recent_pages: int = 1, k_scales=None, unit_status=None, stream=None):
+                 recent_pages: int = 1, k_scales=None, workspace=None, unit_status=None, stream=None):
     """List the pages each (request, KV head) attends: selected int32
     [B][Hkv][top_pages] receives logical page numbers in ascending order, -1
     past a shorter context's last.  q bf16 [B][Hq][128]; bounds and
     bound_scales from page_key_bounds; k_scales float32 [pages][Hkv] for a
     cache with scales per block.  The first sink_pages and last recent_pages
-    pages are always listed.  unit_status: optional int32 [B][Hkv]."""
+    pages are always listed.  unit_status: optional int32 [B][Hkv].  Returns
+    the workspace used (allocated with torch when not given and needed)."""
     import torch
-    dev = q.device
+    dev = q.get_device()
     B, Hq, D = q.shape
     pages, Hkv = bound_scales.shape
     maxp, top = block_tables.shape[1], selected.shape[2]
+    nbytes = 0
+    if workspace is None:
+        nbytes = (_lib or load()).pfkv_select_pages_workspace_size(B, Hkv, maxp)
+        if nbytes:
+            workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
+            if stream is not None:  # a caller that drops it gives it back while that stream may still use it
+                workspace.record_stream(stream)
+    else:
+        nbytes = workspace.numel()
     _call("select_pages", dev, stream, _want("selected", selected, torch.int32, (B, Hkv, top), dev),
           _want("q", q, torch.bfloat16, (B, Hq, D), dev), _want("bounds", bounds, torch.int8, (pages, Hkv, 2, D), dev),
           _want("bound_scales", bound_scales, torch.float32, (pages, Hkv), dev),
           None if k_scales is None else _want("k_scales", k_scales, torch.float32, (pages, Hkv), dev),
           _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
           _want("context_lens", context_lens, torch.int32, (B,), dev), B, Hq, Hkv, D, int(page_size), pages, top,
-          int(sink_pages), int(recent_pages),
+          int(sink_pages), int(recent_pages), None if workspace is None else _want("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes,
           None if unit_status is None else _want("unit_status", unit_status, torch.int32, (B, Hkv), dev))
+    return workspace
 
 
 def paged_sparse_decode_attn(out, q, k_cache, v_cache, granularity: int, k_scales, v_scales, selected, block_tables,
@@ -293,7 +313,7 @@ def paged_sparse_decode_attn(out, q, k_cache, v_cache, granularity: int, k_scale
     logical pages; entries < 0 are padding).  lse_out: optional float32
     [B][Hq]; unit_status: optional int32 [B][Hkv]."""
     import torch
-    dev = q.device
+    dev = q.get_device()
     B, Hq, D = q.shape
     pages, Hkv, P, _ = k_cache.shape
     maxp, top = block_tables.shape[1], selected.shape[2]
@@ -351,7 +371,7 @@ def paged_decode_attn_scaled(out, q, k_cache, v_cache, granularity: int, k_scale
     pages, Hkv, P, _ = k_cache.shape
     if granularity == SCALE_BLOCK:
         for name, t in (("k_scales", k_scales), ("v_scales", v_scales)):
-            _want(name, t, torch.float32, (pages, Hkv), q.device)
+            _want(name, t, torch.float32, (pages, Hkv), q.get_device())
     if workspace is None:
         n = paged_decode_workspace_size(B, Hq, Hkv, D, kv_split_tokens, max_total_chunks)
         workspace = torch.empty(n, dtype=torch.uint8, device=q.device)

@@ -16,17 +16,27 @@
 // of two, so a score is exact and the same in any order of summation: ties are
 // real ties, and go to the lower page.
 //
-// One cluster of up to 8 CTAs per (request, KV head).  Each CTA scores a
-// contiguous share of the pages (half a warp reads the 256 bytes of a page's
-// bounds; dp4a) and keeps the scores in shared memory as order-preserving
-// 32-bit keys.  The K-th largest key is found by its digits, 8 bits a round:
-// the CTAs' 256-bin histograms are summed through distributed shared memory,
-// one cluster barrier a round.  Pages above it, and the lowest-numbered ones
-// equal to it, are then written in order from prefix sums of the counts.  No
-// score goes to global memory and one launch does it all; large calls are
-// bounded by reading the bounds once, small ones by the chain of rounds.
+// Two stages.  Scores: a warp takes some tens of consecutive pages of one
+// (request, KV head), makes the 8-bit query for itself, and reads the 256 bytes
+// of a page's bounds with half a warp (dp4a, two steps of eight pages in flight
+// per half).  Scores are kept as order-preserving 32-bit keys, 1/64 of the bytes
+// read, beside each warp's smallest and largest.
+// List: one CTA per (request, KV head) finds the K-th largest key and writes the
+// list.  A histogram over 256 equal parts of the scores' range says which part
+// holds it; that part's keys, usually few, are compared with one another, or,
+// where scores repeat, counted by their digits, 8 bits a round.  (Parts of the
+// range spread the shared-memory atomics; a float's leading digits would put most
+// keys into a few bins.)  Pages above the threshold, and the lowest-numbered ones
+// equal to it, are written in order from prefix sums.
+//
+// Few short lists run both stages in one launch: a cluster of 8 CTAs per list
+// scores into its first CTA's shared memory, and that CTA lists.  Otherwise two
+// kernels with the keys in the workspace: the first is spread evenly over all SMs
+// with neighbouring warps on neighbouring heads, so that a page's bounds are read
+// as one run, and the second is resident and waiting when the first ends.
 #include <cuda_bf16.h>
 #include <float.h>
+#include <math.h>
 
 #include "pfkv_internal.h"
 #include "pfkv_ptx.cuh"
@@ -36,263 +46,544 @@ namespace pfkv {
 namespace {
 
 constexpr int kD = 128;
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-constexpr int kBatch = 8;            // pages per half warp and step
-constexpr int kMaxCluster = 8;       // portable cluster size
-constexpr int kMaxShare = 49152;     // pages per CTA: keys of 4 bytes in shared memory
+constexpr int kMaxG = 16;
+constexpr int kScoreWarps = 8;
+constexpr int kBatch = 8;                 // pages per half warp and step
+constexpr int kStep = 2 * kBatch;         // pages per warp and step
+constexpr int kBins = 256;
+constexpr int kMaxListThreads = 1024;
+constexpr int kCluster = 8;                // CTAs of a list in one launch
+constexpr int kFusedPages = 8192;          // keys that such a list may have: 32 KB of shared memory
+constexpr int kCandidates = 512;         // keys compared with one another instead of by digits
+constexpr uint32_t kAlways = 0xFFFFFFFFu;  // key of a page that is listed whatever its score
+constexpr uint32_t kLowest = 0u;           // key of a page outside the pool
+
+// What a warp of the first kernel leaves beside its keys.
+struct __align__(16) Extent {
+  float low, high;  // of the scores
+  int32_t bits;     // errors met
+  int32_t unused;
+};
 
 struct SelectArgs {
   int32_t* selected;  // [B][Hkv][K]
   int32_t* status;    // [B][Hkv] or null
+  uint32_t* keys;     // [B * Hkv][stride]
+  Extent* extents;    // [B * Hkv][chunks]
   const uint16_t* q;
   const int8_t* bounds;
   const float* bound_scales;
   const float* k_scales;  // [pages][Hkv] or null
   const int32_t* block_tables;
   const int32_t* context_lens;
-  int Hq, Hkv, G, P, max_pages, K, sink, recent;
-  int64_t num_pages;
+  int B, Hq, Hkv, G, P, max_pages, K, sink, recent;
+  int chunk, chunks, runs;  // pages per warp of the first kernel; warps, and CTAs, per list
+  int64_t num_pages, stride;
 };
 
 __device__ __forceinline__ uint32_t order_key(float x) {
   const uint32_t u = __float_as_uint(x + 0.f);  // -0 (an underflow) counts as 0
   return u ^ ((u & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
 }
-
-__global__ void __launch_bounds__(kThreads) select_pages_kernel(const SelectArgs a) {
-  extern __shared__ uint32_t keys[];
-  __shared__ uint32_t hist[4][256];
-  __shared__ __align__(16) int8_t qs[2 * kD];  // Q-, then Q+: the order of a page's bounds
-  __shared__ float red_f[kWarps];
-  __shared__ int red_i[kWarps];
-  __shared__ uint64_t red_u[kWarps];
-  __shared__ uint32_t digit_of, above_of, in_bin_of;
-  __shared__ uint32_t totals[3];  // this CTA's keys above the threshold, equal to it, and error bits
-
-  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
-  const int nc = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
-  const int64_t unit = blockIdx.x / nc;
-  const int b = (int)(unit / a.Hkv), h = (int)(unit % a.Hkv);
-  int32_t* const out = a.selected + unit * a.K;
-
-  int bits = 0;
-  int L = a.context_lens[b];
-  const int cap = a.max_pages * a.P;
-  if (L < 0 || L > cap) {
-    bits = kErrBadContext;
-    L = L < 0 ? 0 : cap;
-  }
-  const int npages = (L + a.P - 1) / a.P;
-  if (npages <= a.K) {  // every page is listed (the whole cluster takes this path)
-    if (rank == 0) {
-      for (int i = tid; i < a.K; i += kThreads) out[i] = i < npages ? i : -1;
-      if (a.status && tid == 0) a.status[unit] = bits;
-    }
-    return;
-  }
-  const int share = (npages + nc - 1) / nc;
-  const int first = min(rank * share, npages), count = min(share, npages - first);
-
-  // ---------------- the group's query in 8-bit whole numbers
-  for (int i = tid; i < 4 * 256; i += kThreads) hist[i >> 8][i & 255] = 0;
-  {
-    const uint16_t* qp = a.q + ((int64_t)b * a.Hq + (int64_t)h * a.G) * kD + tid;
-    float m = 0.f;
-    if (tid < kD)
-      for (int g = 0; g < a.G; ++g) m = fmaxf(m, fabsf(bf16_lo(qp[g * kD])));
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-    if (lane == 0) red_f[warp] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(red_f[0], red_f[1]), fmaxf(red_f[2], red_f[3]));  // warps 0-3 hold the 128 channels
-    int e = 0;
-    frexpf(fminf(m, FLT_MAX), &e);
-    int sp = 0, sn = 0;
-    if (tid < kD)
-      for (int g = 0; g < a.G; ++g) {
-        const float x = rintf(ldexpf(bf16_lo(qp[g * kD]), 14 - e));
-        const int n = (int)fminf(fmaxf(x, -16384.f), 16384.f);
-        sp += max(n, 0);
-        sn += min(n, 0);
-      }
-    int most = max(sp, -sn);
-    most = __reduce_max_sync(0xFFFFFFFFu, most);
-    if (lane == 0) red_i[warp] = most;
-    __syncthreads();
-    most = max(max(red_i[0], red_i[1]), max(red_i[2], red_i[3]));
-    int j = 0;
-    while ((127 << j) < most) ++j;
-    if (tid < kD) {  // S < 2^24 and the power of two: exact until the rounding
-      qs[tid] = (int8_t)__float2int_rn(ldexpf((float)sn, -j));
-      qs[kD + tid] = (int8_t)__float2int_rn(ldexpf((float)sp, -j));
-    }
-    __syncthreads();
-  }
-
-  // ---------------- scores of this CTA's pages
-  {
-    const int l16 = lane & 15, hw = tid >> 4;  // half warp of the CTA
-    const uint4 qv = *reinterpret_cast<const uint4*>(qs + 16 * l16);
-    const int own = l16 >> 1;  // the page of the eight whose sum this lane ends up with
-    const int32_t* table = a.block_tables + (int64_t)b * a.max_pages + first;
-    constexpr int kStep = kThreads / 16 * kBatch;
-    int next = -1;
-    if (hw * kBatch + own < count) next = __ldg(table + hw * kBatch + own);
-    for (int i0 = hw * kBatch; i0 - hw * kBatch < count; i0 += kStep) {
-      const int i = i0 + own;
-      int page = next;
-      next = i + kStep < count ? __ldg(table + i + kStep) : -1;
-      const bool there = i < count;
-      if (there && (page < 0 || (int64_t)page >= a.num_pages)) bits |= kErrBadPage;
-      const bool ok = there && page >= 0 && (int64_t)page < a.num_pages;
-      const int64_t at = ok ? (int64_t)page * a.Hkv + h : 0;  // entry 0 stands in for one that is not there
-      float scale = 0.f;
-      if (!(l16 & 1)) {
-        scale = __ldg(a.bound_scales + at);
-        if (a.k_scales) scale *= __ldg(a.k_scales + at);
-      }
-      uint4 v[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u) {
-        const int64_t pu = __shfl_sync(0xFFFFFFFFu, at, 2 * u, 16);
-        v[u] = __ldg(reinterpret_cast<const uint4*>(a.bounds + pu * (2 * kD)) + l16);
-      }
-      int s[kBatch];
-#pragma unroll
-      for (int u = 0; u < kBatch; ++u)
-        s[u] = __dp4a((int)v[u].x, (int)qv.x,
-                      __dp4a((int)v[u].y, (int)qv.y, __dp4a((int)v[u].z, (int)qv.z, __dp4a((int)v[u].w, (int)qv.w, 0))));
-      // sums over the 16 lanes, each step halving the pages a lane holds: page
-      // `own` ends in lanes 2 own and 2 own + 1
-      int s4[4], s2[2];
-#pragma unroll
-      for (int u = 0; u < 4; ++u)
-        s4[u] = ((l16 & 8) ? s[u + 4] : s[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 8) ? s[u] : s[u + 4], 8);
-#pragma unroll
-      for (int u = 0; u < 2; ++u)
-        s2[u] = ((l16 & 4) ? s4[u + 2] : s4[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 4) ? s4[u] : s4[u + 2], 4);
-      int sum = ((l16 & 2) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 2) ? s2[0] : s2[1], 2);
-      sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-      if (there && !(l16 & 1)) {
-        uint32_t key = ok ? order_key((float)sum * scale) : 0u;
-        const int index = first + i;
-        if (index < a.sink || index >= npages - a.recent) key = 0xFFFFFFFFu;  // above every finite score
-        keys[i] = key;
-      }
-    }
-  }
-  __syncthreads();
-
-  // ---------------- the K-th largest key, digit by digit
-  uint32_t prefix = 0, mask = 0;
-  uint32_t want = (uint32_t)a.K;  // of the keys that agree with the prefix, how many are listed
-#pragma unroll 1
-  for (int p = 0; p < 4; ++p) {
-    const int shift = 24 - 8 * p;
-    for (int i = tid; i < count; i += kThreads) {
-      const uint32_t k = keys[i];
-      if ((k & mask) == prefix) atomicAdd(&hist[p][(k >> shift) & 255], 1u);
-    }
-    __syncwarp();
-    tc::cluster_sync();
-    uint32_t n = 0;
-    const uint32_t mine = smem_u32(&hist[p][tid]);
-    for (int r = 0; r < nc; ++r) n += tc::ld_cluster_u32(tc::mapa(mine, r));
-    // keys in this bin or a higher one
-    uint32_t sum = n;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t x = __shfl_down_sync(0xFFFFFFFFu, sum, o);
-      if (lane + o < 32) sum += x;
-    }
-    if (lane == 0) red_i[warp] = (int)sum;
-    __syncthreads();
-    for (int w = warp + 1; w < kWarps; ++w) sum += (uint32_t)red_i[w];
-    if (sum >= want && sum - n < want) {  // one bin only
-      digit_of = (uint32_t)tid;
-      above_of = sum - n;
-      in_bin_of = n;
-    }
-    __syncthreads();
-    prefix |= digit_of << shift;
-    mask |= 255u << shift;
-    want -= above_of;
-    if (in_bin_of == want) break;  // the whole bin is listed: the same in every CTA
-    __syncthreads();  // digit_of and red_i are written again in the next round
-  }
-
-  // ---------------- the list, in order: each thread a contiguous piece of odd
-  // length (so that the threads' shared-memory reads spread over the banks)
-  const int piece = ((count + kThreads - 1) / kThreads) | 1;
-  const int p0 = min(tid * piece, count), p1 = min(p0 + piece, count);
-  uint32_t gt = 0, eq = 0;
-  for (int i = p0; i < p1; ++i) {
-    const uint32_t k = keys[i] & mask;
-    gt += k > prefix;
-    eq += k == prefix;
-  }
-  const uint64_t own = ((uint64_t)gt << 32) | eq;
-  uint64_t inc = own;
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const uint64_t x = __shfl_up_sync(0xFFFFFFFFu, inc, o);
-    if (lane >= o) inc += x;
-  }
-  if (lane == 31) red_u[warp] = inc;
-  if (tid == 0) totals[2] = 0;
-  __syncthreads();
-  bits = __reduce_or_sync(0xFFFFFFFFu, bits);
-  if (lane == 0 && bits) atomicOr(&totals[2], (uint32_t)bits);
-  uint64_t before = inc - own;
-  for (int w = 0; w < warp; ++w) before += red_u[w];
-  if (tid == kThreads - 1) {
-    const uint64_t all = before + own;
-    totals[0] = (uint32_t)(all >> 32);
-    totals[1] = (uint32_t)all;
-  }
-  __syncwarp();
-  tc::cluster_sync();
-  uint32_t gt_before = (uint32_t)(before >> 32), eq_before = (uint32_t)before, all_bits = 0;
-  const uint32_t t0 = smem_u32(totals);
-  for (int r = 0; r < nc; ++r) {
-    const uint32_t at = tc::mapa(t0, r);
-    if (r < rank) {
-      gt_before += tc::ld_cluster_u32(at);
-      eq_before += tc::ld_cluster_u32(at + 4);
-    }
-    all_bits |= tc::ld_cluster_u32(at + 8);
-  }
-  for (int i = p0; i < p1; ++i) {
-    const uint32_t k = keys[i] & mask;
-    const bool above = k > prefix, equal = k == prefix;
-    if (above || (equal && eq_before < want)) out[gt_before + min(eq_before, want)] = first + i;
-    gt_before += above;
-    eq_before += equal;
-  }
-  if (a.status && rank == 0 && tid == 0) a.status[unit] = (int32_t)all_bits;
-  __syncwarp();
-  tc::cluster_sync();  // no CTA leaves while another may still read its shared memory
+__device__ __forceinline__ float unordered(uint32_t key) {
+  return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
-// CTAs per (request, KV head): enough clusters' CTAs for about two on every
-// SM, as long as a CTA keeps at least 256 pages to score; more where a share
-// would not fit in shared memory.
-int cluster_size(int64_t units, int max_pages, int sms) {
-  int c = 1;
-  while (c < kMaxCluster && units * c < 2 * (int64_t)sms && max_pages / (2 * c) >= 256) c *= 2;
-  while (c < kMaxCluster && (max_pages + c - 1) / c > kMaxShare) c *= 2;
+// The cluster's barrier in two halves, by every thread of the cluster.
+__device__ __forceinline__ void cluster_arrive() {
+  __syncwarp();
+  asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory");
+}
+__device__ __forceinline__ void cluster_wait() {
+  __syncwarp();
+  asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
+// Generic address of the same shared array in the cluster's first CTA.
+template <class T>
+__device__ __forceinline__ T* map_to_first(T* p) {
+  uint64_t r;
+  asm("mapa.u64 %0, %1, 0;" : "=l"(r) : "l"(p));
+  return reinterpret_cast<T*>(r);
+}
+
+__device__ __forceinline__ float warp_min(float x) {
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) x = fminf(x, __shfl_xor_sync(0xFFFFFFFFu, x, o));
+  return x;
+}
+
+// Pages of request b's context; *bits: a length outside the table is clamped.
+__device__ __forceinline__ int pages_of(const SelectArgs& a, int b, int* bits) {
+  int L = a.context_lens[b];
+  const int cap = a.max_pages * a.P;
+  *bits = 0;
+  if (L < 0 || L > cap) {
+    *bits = kErrBadContext;
+    L = L < 0 ? 0 : cap;
+  }
+  return (L + a.P - 1) / a.P;
+}
+
+// ------------------------------------------------------------------- scores
+struct ScoreShared {
+  __align__(16) int8_t q[2 * kD];  // Q-, then Q+: the order of a page's bounds
+  uint32_t largest[4], most[4];
+};
+
+// The pages first .. first + 8 chunk - 1 of (b, h) by one CTA, chunk to a warp:
+// keys to keys[page] and each warp's extent to extents[page / chunk], in global
+// memory or in a cluster CTA's shared memory; `ready` is called by every thread
+// before the first write.  False, and nothing done, where every page is listed.
+// What does not depend on the length or the query is loaded ahead of them: the
+// chain is block table -> bounds, and the query is made while those arrive.
+template <class Ready>
+__device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh, int64_t b, int h, int first,
+                                            int chunk, uint32_t* keys, Extent* extents, Ready ready) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int l16 = lane & 15, half = lane >> 4;
+  const int own = l16 >> 1;  // the page of the half warp's eight whose sum this lane ends up with
+  first += warp * chunk;
+  const int32_t* table = a.block_tables + b * a.max_pages + first;
+  const int room = min(chunk, a.max_pages - first);
+  auto entry = [&](int i) { return i < room ? __ldg(table + i) : -1; };
+  int i = half * kBatch + own;
+  const int page0 = entry(i);
+  int next = entry(i + kStep);
+  // thread d < 128: channel d of the group's rows
+  uint32_t row[kMaxG];
+  {
+    const uint16_t* q = a.q + (b * a.Hq + (int64_t)h * a.G) * kD + tid;
+#pragma unroll
+    for (int g = 0; g < kMaxG; ++g) row[g] = tid < kD && g < a.G ? __ldg(q + g * kD) : 0u;
+  }
+  int bits;
+  const int npages = pages_of(a, (int)b, &bits);
+  if (npages <= a.K) return false;
+  const int count = max(min(chunk, npages - first), 0);
+
+  struct Step {
+    uint4 v[kBatch];
+    float scale;
+    bool ok;
+  };
+  float low = INFINITY, high = -INFINITY;
+  auto load = [&](Step& st, int i, int page) {
+    st.ok = page >= 0 && (int64_t)page < a.num_pages;
+    if (i < count && !st.ok) bits |= kErrBadPage;
+    const int at = st.ok ? page * a.Hkv + h : 0;  // entry 0 stands in for one that is not there
+    st.scale = __ldg(a.bound_scales + at);
+    if (a.k_scales) st.scale *= __ldg(a.k_scales + at);
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u) {
+      const int pu = __shfl_sync(0xFFFFFFFFu, at, 2 * u, 16);
+      st.v[u] = __ldg(reinterpret_cast<const uint4*>(a.bounds) + (int64_t)pu * (2 * kD / 16) + l16);
+    }
+  };
+  Step x, y;
+  load(x, i, page0);
+
+  // ---------------- the group's query in 8-bit whole numbers
+  uint32_t largest = 0;
+#pragma unroll
+  for (int g = 0; g < kMaxG; ++g) largest = max(largest, row[g] & 0x7FFFu);
+  largest = __reduce_max_sync(0xFFFFFFFFu, largest);
+  if (tid < kD && lane == 0) sh.largest[warp] = largest;
+  __syncthreads();
+  largest = max(max(sh.largest[0], sh.largest[1]), max(sh.largest[2], sh.largest[3]));
+  // 2^(e-1) <= largest < 2^e: by the exponent, or a subnormal's leading bit
+  const int e = largest >= 0x7F80u ? 128 : (largest >> 7 ? (int)(largest >> 7) - 126 : (largest ? -101 - __clz((int)largest) : 0));
+  // 2^(14 - e) in two exact factors: it can leave fp32's range, its halves cannot
+  const int h1 = (14 - e) / 2, h2 = 14 - e - h1;
+  const float f1 = __uint_as_float((uint32_t)(127 + h1) << 23), f2 = __uint_as_float((uint32_t)(127 + h2) << 23);
+  // S+ and -S-: magnitudes, because nvcc 13.0 was seen to drop the sign in
+  // max(most, max(sp, -sn)) of whole numbers
+  uint32_t sp = 0, sm = 0;
+#pragma unroll
+  for (int g = 0; g < kMaxG; ++g) {
+    const float n = fminf(fmaxf(rintf(__uint_as_float(row[g] << 16) * f1 * f2), -16384.f), 16384.f);
+    sp += (uint32_t)fmaxf(n, 0.f);
+    sm += (uint32_t)fmaxf(-n, 0.f);
+  }
+  uint32_t most = __reduce_max_sync(0xFFFFFFFFu, max(sp, sm));
+  if (tid < kD && lane == 0) sh.most[warp] = most;
+  __syncthreads();
+  most = max(max(sh.most[0], sh.most[1]), max(sh.most[2], sh.most[3]));
+  int j = 0;
+  while ((127u << j) < most) ++j;
+  const float f = __uint_as_float((uint32_t)(127 - j) << 23);  // 2^-j
+  if (tid < kD) {  // below 2^24 and a power of two: exact until the rounding
+    sh.q[tid] = (int8_t)-__float2int_rn((float)sm * f);
+    sh.q[kD + tid] = (int8_t)__float2int_rn((float)sp * f);
+  }
+  __syncthreads();
+  const uint4 qv = *reinterpret_cast<const uint4*>(sh.q + 16 * l16);
+  ready();
+  if (count == 0) return true;
+
+  // ---------------- the warp's pages, two steps of loads in flight
+  auto sum_up = [&](const Step& st, int i) {
+    int s[kBatch];
+#pragma unroll
+    for (int u = 0; u < kBatch; ++u)
+      s[u] = __dp4a((int)st.v[u].x, (int)qv.x,
+                    __dp4a((int)st.v[u].y, (int)qv.y,
+                           __dp4a((int)st.v[u].z, (int)qv.z, __dp4a((int)st.v[u].w, (int)qv.w, 0))));
+    // sums over the 16 lanes, each step halving the pages a lane holds: page
+    // `own` ends in lanes 2 own and 2 own + 1
+    int s4[4], s2[2];
+#pragma unroll
+    for (int u = 0; u < 4; ++u)
+      s4[u] = ((l16 & 8) ? s[u + 4] : s[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 8) ? s[u] : s[u + 4], 8);
+#pragma unroll
+    for (int u = 0; u < 2; ++u)
+      s2[u] = ((l16 & 4) ? s4[u + 2] : s4[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 4) ? s4[u] : s4[u + 2], 4);
+    int sum = ((l16 & 2) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 2) ? s2[0] : s2[1], 2);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    if (i < count && !(l16 & 1)) {
+      uint32_t key = kLowest;
+      const int index = first + i;
+      if (index < a.sink || index >= npages - a.recent) {
+        key = kAlways;
+      } else if (st.ok) {
+        const float x = (float)sum * st.scale;
+        low = fminf(low, x);
+        high = fmaxf(high, x);
+        key = order_key(x);
+      }
+      keys[index] = key;
+    }
+  };
+  for (int done = 0; done < count; done += 2 * kStep) {
+    int page = next;
+    next = entry(i + 2 * kStep);
+    load(y, i + kStep, page);
+    sum_up(x, i);
+    page = next;
+    next = entry(i + 3 * kStep);
+    load(x, i + 2 * kStep, page);
+    sum_up(y, i + kStep);
+    i += 2 * kStep;
+  }
+  low = warp_min(low);
+  high = -warp_min(-high);
+  bits = (int)__reduce_or_sync(0xFFFFFFFFu, (unsigned)bits);
+  if (lane == 0) extents[first / chunk] = Extent{low, high, bits, 0};
+  return true;
+}
+
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) score_pages_kernel(const SelectArgs a) {
+  __shared__ ScoreShared sh;
+  grid_launch_dependents();  // the listing kernel may take its place and wait
+  const int h = (int)(blockIdx.x % a.Hkv);  // neighbouring CTAs: neighbouring heads of the same pages
+  const int64_t br = blockIdx.x / a.Hkv;
+  const int run = (int)(br % a.runs);
+  const int64_t b = br / a.runs, unit = b * a.Hkv + h;
+  const int first = run * kScoreWarps * a.chunk;
+  if ((int64_t)first * a.P >= a.context_lens[b]) return;
+  score_block(a, sh, b, h, first, a.chunk, a.keys + unit * a.stride, a.extents + unit * a.chunks, [] {});
+}
+
+// --------------------------------------------------------------------- lists
+// Sum of x over this thread and later ones of the block's first kBins threads
+// (others pass 0 and get no answer).
+__device__ __forceinline__ uint32_t suffix_sum(uint32_t x, uint32_t* red) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_down_sync(0xFFFFFFFFu, x, o);
+    if (lane + o < 32) x += y;
+  }
+  if (warp < kBins / 32 && lane == 0) red[warp] = x;
+  __syncthreads();
+#pragma unroll
+  for (int w = 1; w < kBins / 32; ++w) x += w > warp ? red[w] : 0u;
+  return x;
+}
+
+struct ListShared {
+  uint32_t hist[5][kBins];  // of parts of the range, then of four digits
+  uint2 cand[kCandidates];  // keys of the part, and which warp's they are
+  uint32_t above[kMaxListThreads / 32], equal[kMaxListThreads / 32];  // listed keys of each warp's piece
+  float range[2][kMaxListThreads / 32];
+  uint32_t bins[kBins / 32];
+  uint32_t found[5];
+  uint32_t err;
+};
+
+// Every page is listed: a CTA writes them.
+__device__ __forceinline__ void list_all(const SelectArgs& a, int64_t unit, int npages, int bits) {
+  for (int i = threadIdx.x; i < a.K; i += blockDim.x) a.selected[unit * a.K + i] = i < npages ? i : -1;
+  if (a.status && threadIdx.x == 0) a.status[unit] = bits;
+}
+
+// One CTA: the list of `unit` from its npages > K keys (16-byte aligned) and the
+// nchunks extents of their scores; `ready` is called before they are read.
+template <class Ready>
+__device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, int64_t unit, int npages,
+                                          const uint32_t* keys, const Extent* extents, int nchunks, int bits,
+                                          Ready ready) {
+  const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
+  const int threads = blockDim.x, warps = threads >> 5;
+  int32_t* const out = a.selected + unit * a.K;
+  for (int i = tid; i < 5 * kBins; i += threads) sh.hist[i / kBins][i % kBins] = 0;
+  if (lane == 0) sh.above[warp] = sh.equal[warp] = 0;
+  if (tid == 0) {
+    sh.found[3] = 0;
+    sh.err = 0;
+  }
+  // keys: each warp a contiguous piece, 128 at a time, four to a lane
+  const int piece = ((npages + warps - 1) / warps + 127) & ~127;
+  const int p0 = min(warp * piece, npages), p1 = min(p0 + piece, npages);
+  // fn(first index, four keys, how many of them there are); whole warps
+  auto each = [&](auto&& fn) {
+#pragma unroll 1
+    for (int i = p0 + 4 * lane; i - 4 * lane < p1; i += 128) {
+      const int n = max(min(p1 - i, 4), 0);
+      fn(i, n > 0 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0u, 0u, 0u, 0u), n);
+    }
+  };
+  ready();
+
+  float low = INFINITY, high = -INFINITY;
+  for (int i = tid; i < nchunks; i += threads) {
+    const Extent e = extents[i];
+    low = fminf(low, e.low);
+    high = fmaxf(high, e.high);
+    bits |= e.bits;
+  }
+  low = warp_min(low);
+  high = -warp_min(-high);
+  bits = (int)__reduce_or_sync(0xFFFFFFFFu, (unsigned)bits);
+  if (lane == 0) {
+    sh.range[0][warp] = low;
+    sh.range[1][warp] = high;
+  }
+  __syncthreads();
+  if (lane == 0 && bits) atomicOr(&sh.err, (uint32_t)bits);
+  low = warp_min(lane < warps ? sh.range[0][lane] : INFINITY);
+  high = -warp_min(lane < warps ? -sh.range[1][lane] : INFINITY);
+
+  // ---------------- which of 256 equal parts of the scores' range holds the
+  // K-th largest; equal scores, or a range that is no number: one part
+  float per = (float)kBins / (high - low);
+  if (!(high > low) || !isfinite(per)) per = 0.f;
+  auto part_of = [&](uint32_t key) {
+    if (key == kAlways) return kBins - 1;
+    return min(max(__float2int_rd((unordered(key) - low) * per), 0), kBins - 1);  // grows with the key; NaN: 0
+  };
+  each([&](int, const uint4& k, int n) {
+    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) atomicAdd(&sh.hist[0][part_of(w[c])], 1u);
+  });
+  uint32_t want = (uint32_t)a.K;  // of the keys of the part, how many are listed
+  // the bin that holds the want-th largest, by the block's first 256 threads
+  auto find = [&](const uint32_t* bins) {
+    __syncthreads();
+    const uint32_t n = tid < kBins ? bins[tid] : 0u;
+    const uint32_t sum = suffix_sum(n, sh.bins);
+    if (tid < kBins && sum >= want && sum - n < want) {  // one bin only
+      sh.found[0] = (uint32_t)tid;
+      sh.found[1] = sum - n;
+      sh.found[2] = n;
+    }
+    __syncthreads();
+    want -= sh.found[1];
+  };
+  find(sh.hist[0]);
+  const int part = (int)sh.found[0];
+  const uint32_t in_part = sh.found[2];
+
+  // ---------------- the threshold: listed are the keys of higher parts, those
+  // of the part with (key & mask) > edge, and the first `want` with == edge;
+  // sh.above and sh.equal count the former and the latter in each warp's piece
+  uint32_t edge = 0, mask = 0xFFFFFFFFu;
+  if (in_part <= kCandidates) {  // few: compared with one another
+    uint32_t above = 0;
+    each([&](int, const uint4& k, int n) {
+      const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) {
+          const int at = part_of(w[c]);
+          above += at > part;
+          if (at == part) sh.cand[atomicAdd(&sh.found[3], 1u)] = make_uint2(w[c], (uint32_t)warp);
+        }
+    });
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    if (lane == 0) sh.above[warp] = above;
+    __syncthreads();
+    for (uint32_t i = tid; i < in_part; i += threads) {
+      const uint32_t k = sh.cand[i].x;
+      uint32_t gt = 0, eq = 0;
+      for (uint32_t j = 0; j < in_part; ++j) {
+        const uint32_t o = sh.cand[j].x;
+        gt += o > k;
+        eq += o == k;
+      }
+      if (gt + eq < want) {  // above the want-th largest
+        atomicAdd(&sh.above[sh.cand[i].y], 1u);
+      } else if (gt < want) {  // equal to it: all of these write the same
+        atomicAdd(&sh.equal[sh.cand[i].y], 1u);
+        sh.found[0] = k;
+        sh.found[4] = want - gt;
+      }
+    }
+    __syncthreads();
+    edge = sh.found[0];
+    want = sh.found[4];
+  } else {  // many, as where scores repeat: by their digits of 8 bits
+    mask = 0;
+#pragma unroll 1
+    for (int p = 1; p <= 4; ++p) {
+      const int shift = 32 - 8 * p;
+      each([&](int, const uint4& k, int n) {
+        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+          if (c < n && (w[c] & mask) == edge && part_of(w[c]) == part)
+            atomicAdd(&sh.hist[p][(w[c] >> shift) & 255], 1u);
+      });
+      find(sh.hist[p]);
+      edge |= sh.found[0] << shift;
+      mask |= 255u << shift;
+      if (sh.found[2] == want) break;  // all of them are listed
+    }
+  }
+  // 2: above the threshold, 1: equal to it, 0: below
+  auto place = [&](uint32_t k) {
+    const int at = part_of(k);
+    if (at != part) return at > part ? 2 : 0;
+    return (k & mask) > edge ? 2 : ((k & mask) == edge ? 1 : 0);
+  };
+  if (in_part > kCandidates) {
+    uint32_t above = 0, equal = 0;
+    each([&](int, const uint4& k, int n) {
+      const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) {
+          above += place(w[c]) == 2;
+          equal += place(w[c]) == 1;
+        }
+    });
+    above = __reduce_add_sync(0xFFFFFFFFu, above);
+    equal = __reduce_add_sync(0xFFFFFFFFu, equal);
+    if (lane == 0) {
+      sh.above[warp] = above;
+      sh.equal[warp] = equal;
+    }
+    __syncthreads();
+  }
+
+  // ---------------- the list, in order
+  uint32_t above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.above[lane] : 0u);  // in earlier warps' pieces
+  uint32_t equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.equal[lane] : 0u);
+  const uint32_t below = (1u << lane) - 1;
+  each([&](int i, const uint4& k, int n) {
+    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+    int c[4];
+    uint32_t a2 = above, e2 = equal;  // before this lane's four
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      c[u] = u < n ? place(w[u]) : 0;
+      const uint32_t m2 = __ballot_sync(0xFFFFFFFFu, c[u] == 2), m1 = __ballot_sync(0xFFFFFFFFu, c[u] == 1);
+      a2 += __popc(m2 & below);
+      e2 += __popc(m1 & below);
+      above += __popc(m2);
+      equal += __popc(m1);
+    }
+#pragma unroll
+    for (int u = 0; u < 4; ++u) {
+      if (c[u] == 2 || (c[u] == 1 && e2 < want)) out[a2 + min(e2, want)] = i + u;
+      a2 += c[u] == 2;
+      e2 += c[u] == 1;
+    }
+  });
+  if (a.status && tid == 0) a.status[unit] = (int32_t)sh.err;
+}
+
+__global__ void __launch_bounds__(kMaxListThreads, 1) list_pages_kernel(const SelectArgs a) {
+  __shared__ ListShared sh;
+  const int64_t unit = blockIdx.x;
+  int bits;
+  const int npages = pages_of(a, (int)(unit / a.Hkv), &bits);
+  if (npages <= a.K) {
+    grid_dependency_wait();
+    list_all(a, unit, npages, bits);
+    return;
+  }
+  list_unit(a, sh, unit, npages, a.keys + unit * a.stride, a.extents + unit * a.chunks,
+            (npages + a.chunk - 1) / a.chunk, bits, [] { grid_dependency_wait(); });  // the scores are visible
+}
+
+// ------------------------------------------------------- both stages at once
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps * 32, 2)
+    select_pages_kernel(const SelectArgs a) {
+  __shared__ ListShared sh;
+  __shared__ ScoreShared ssh;
+  __shared__ __align__(16) uint32_t keys[kFusedPages];
+  __shared__ Extent extents[kCluster * kScoreWarps];
+  const int rank = (int)tc::cluster_ctarank();
+  const int64_t unit = blockIdx.x / kCluster, b = unit / a.Hkv;
+  int bits;
+  const int npages = pages_of(a, (int)b, &bits);
+  if (npages <= a.K) {  // the whole cluster takes this path
+    if (rank == 0) list_all(a, unit, npages, bits);
+    return;
+  }
+  // even chunks, a multiple of what a warp takes at once
+  const int per = (npages + kCluster * kScoreWarps - 1) / (kCluster * kScoreWarps);
+  const int chunk = (per + kStep - 1) / kStep * kStep;
+  cluster_arrive();  // this CTA is running: its shared memory may be written
+  // the first CTA's arrays, as this CTA sees them
+  score_block(a, ssh, b, (int)(unit % a.Hkv), rank * kScoreWarps * chunk, chunk, map_to_first(keys),
+              map_to_first(extents), [] { cluster_wait(); });
+  cluster_arrive();
+  if (rank != 0) {
+    cluster_wait();
+    return;
+  }
+  list_unit(a, sh, unit, npages, keys, extents, (npages + chunk - 1) / chunk, bits, [] { cluster_wait(); });
+}
+
+// One launch while all its clusters are resident at once.
+bool one_launch(int64_t units, int max_pages, int sms) {
+  return max_pages <= kFusedPages && units * kCluster <= 2 * (int64_t)sms;
+}
+
+// Pages per warp of the first kernel: about four warps a scheduler on every SM,
+// and at least the step that a warp takes at once.
+int pages_per_warp(int64_t pairs, int sms) {
+  const int64_t even = pairs / ((int64_t)sms * 24);
+  int c = kStep;
+  while (c < 256 && c < even) c *= 2;
   return c;
 }
 
+size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
+size_t keys_bytes(int64_t units, int64_t stride) { return align_up((size_t)units * (size_t)stride * 4); }
+int64_t stride_of(int max_pages) { return ((int64_t)max_pages + 63) / 64 * 64; }
+
 }  // namespace
 }  // namespace pfkv
+
+extern "C" size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq) {
+  if (batch < 0 || num_kv_heads <= 0 || max_pages_per_seq <= 0) return 0;
+  const int64_t units = (int64_t)batch * num_kv_heads;
+  if (pfkv::one_launch(units, max_pages_per_seq, pfkv::device_sm_count())) return 0;
+  const int64_t chunks = ((int64_t)max_pages_per_seq + pfkv::kStep - 1) / pfkv::kStep;
+  return pfkv::keys_bytes(units, pfkv::stride_of(max_pages_per_seq)) +
+         pfkv::align_up((size_t)units * (size_t)chunks * sizeof(pfkv::Extent)) + 256;
+}
 
 extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t* bounds, const float* bound_scales,
                                  const float* k_scales, const int32_t* block_tables, int max_pages_per_seq,
                                  const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads,
                                  int head_dim, int page_size, int64_t num_pages, int top_pages, int sink_pages,
-                                 int recent_pages, int32_t* unit_status, pfkv_stream_t stream) {
+                                 int recent_pages, void* workspace, size_t workspace_bytes, int32_t* unit_status,
+                                 pfkv_stream_t stream) {
   using namespace pfkv;
   clear_error();
   if (batch < 0 || num_q_heads <= 0 || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 || num_pages <= 0 ||
@@ -303,30 +594,37 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   if ((int64_t)sink_pages + recent_pages > top_pages)
     return fail(PFKV_ERR_INVALID_ARG, "select_pages: sink_pages + recent_pages > top_pages");
   const int G = num_q_heads / num_kv_heads;
-  if (G > 16) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: group size %d > 16", G);
+  if (G > kMaxG) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: group size %d > 16", G);
   if (head_dim != kD) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: head_dim %d != 128", head_dim);
   if ((int64_t)max_pages_per_seq * page_size >= (int64_t)1 << 30)
     return fail(PFKV_ERR_UNSUPPORTED, "select_pages: block table too long");
-  if (max_pages_per_seq > kMaxCluster * kMaxShare)
-    return fail(PFKV_ERR_UNSUPPORTED, "select_pages: more than %d pages per request", kMaxCluster * kMaxShare);
+  if (num_pages > ((int64_t)1 << 31) / num_kv_heads - 1)
+    return fail(PFKV_ERR_UNSUPPORTED, "select_pages: 2^31 or more (page, KV head) pairs");
   const int64_t units = (int64_t)batch * num_kv_heads;
-  if (units > 0x7FFFFFFF / kMaxCluster) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: batch too large");
+  if (units > 0x7FFFFFFF) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: batch too large");
   if (batch == 0) return PFKV_OK;
-  if (!selected || !q || !bounds || !bound_scales || !block_tables || !context_lens)
+  const size_t need = pfkv_select_pages_workspace_size(batch, num_kv_heads, max_pages_per_seq);
+  if (!selected || !q || !bounds || !bound_scales || !block_tables || !context_lens || (need > 0 && !workspace))
     return fail(PFKV_ERR_INVALID_ARG, "select_pages: null pointer");
   if (!aligned(q, 16) || !aligned(bounds, 16) || !aligned(selected, 4) || !aligned(bound_scales, 4) ||
       (k_scales && !aligned(k_scales, 4)) || !aligned(block_tables, 4) || !aligned(context_lens, 4) ||
-      (unit_status && !aligned(unit_status, 4)))
+      !aligned(workspace, 256) || (unit_status && !aligned(unit_status, 4)))
     return fail(PFKV_ERR_INVALID_ARG, "select_pages: misaligned pointer");
+  if (workspace_bytes < need)
+    return fail(PFKV_ERR_WORKSPACE, "select_pages: workspace of %zu bytes is too small", workspace_bytes);
   SelectArgs a;
   a.selected = selected;
   a.status = unit_status;
+  a.stride = stride_of(max_pages_per_seq);
+  a.keys = static_cast<uint32_t*>(workspace);
+  a.extents = reinterpret_cast<Extent*>(static_cast<uint8_t*>(workspace) + keys_bytes(units, a.stride));
   a.q = static_cast<const uint16_t*>(q);
   a.bounds = bounds;
   a.bound_scales = bound_scales;
   a.k_scales = k_scales;
   a.block_tables = block_tables;
   a.context_lens = context_lens;
+  a.B = batch;
   a.Hq = num_q_heads;
   a.Hkv = num_kv_heads;
   a.G = G;
@@ -336,24 +634,33 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   a.sink = sink_pages;
   a.recent = recent_pages;
   a.num_pages = num_pages;
-  const int c = cluster_size(units, max_pages_per_seq, device_sm_count());
-  const int smem = (max_pages_per_seq + c - 1) / c * 4;
-  static std::atomic<uint64_t> smem_set{0};
-  const int rc = set_max_dynamic_smem(reinterpret_cast<const void*>(select_pages_kernel), kMaxShare * 4, smem_set,
-                                      "select_pages set smem attribute");
-  if (rc != PFKV_OK) return rc;
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  const int sms = device_sm_count();
+  if (one_launch(units, max_pages_per_seq, sms)) {
+    select_pages_kernel<<<(unsigned)(units * kCluster), kScoreWarps * 32, 0, s>>>(a);
+    return check_cuda("select_pages launch");
+  }
+  a.chunk = pages_per_warp(units * max_pages_per_seq, sms);
+  a.chunks = (max_pages_per_seq + a.chunk - 1) / a.chunk;
+  a.runs = (a.chunks + kScoreWarps - 1) / kScoreWarps;
+  const int64_t blocks = units * a.runs;
+  if (blocks > 0x7FFFFFFF) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: too many pages");
+  score_pages_kernel<<<(unsigned)blocks, kScoreWarps * 32, 0, s>>>(a);
+  // the listing kernel is launched as a programmatic dependent: its CTAs wait
+  // (griddepcontrol.wait) for the scores.  A list's threads: as many as its
+  // keys keep busy while all lists are resident together
+  int threads = kBins;
+  while (threads < kMaxListThreads && threads * 4 < max_pages_per_seq && units * 2 * threads <= (int64_t)sms * 2048)
+    threads *= 2;
   cudaLaunchAttribute attr[1];
-  attr[0].id = cudaLaunchAttributeClusterDimension;
-  attr[0].val.clusterDim.x = (unsigned)c;
-  attr[0].val.clusterDim.y = 1;
-  attr[0].val.clusterDim.z = 1;
+  attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  attr[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3((unsigned)(units * c));
-  cfg.blockDim = dim3(kThreads);
-  cfg.dynamicSmemBytes = (size_t)smem;
-  cfg.stream = reinterpret_cast<cudaStream_t>(stream);
+  cfg.gridDim = dim3((unsigned)units);
+  cfg.blockDim = dim3((unsigned)threads);
+  cfg.stream = s;
   cfg.attrs = attr;
   cfg.numAttrs = 1;
-  if (cudaLaunchKernelEx(&cfg, select_pages_kernel, a) != cudaSuccess) return check_cuda("select_pages launch");
+  if (cudaLaunchKernelEx(&cfg, list_pages_kernel, a) != cudaSuccess) return check_cuda("select_pages launch");
   return check_cuda("select_pages launch");
 }

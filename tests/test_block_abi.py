@@ -60,10 +60,10 @@ def test_bounds_host_validation(lib):
 
 
 def test_select_host_validation(lib):
-    def call(B=2, Hq=16, Hkv=2, D=128, P=16, pages=64, maxp=8, top=4, sink=1, recent=1, sel=_fake(), ks=None, st=None,
-             q=_fake()):
+    def call(B=2, Hq=16, Hkv=2, D=128, P=16, pages=64, maxp=9000, top=4, sink=1, recent=1, sel=_fake(), ks=None, st=None,
+             q=_fake(), ws=_fake(), wsb=1 << 20):
         return lib.pfkv_select_pages(sel, q, _fake(), _fake(), ks, _fake(), maxp, _fake(), B, Hq, Hkv, D, P, i64(pages),
-                                     top, sink, recent, st, None)
+                                     top, sink, recent, ws, wsb, st, None)
 
     for bad in (dict(B=-1), dict(Hkv=0), dict(P=0), dict(pages=0), dict(maxp=0), dict(top=0), dict(sink=-1),
                 dict(recent=-1)):
@@ -72,8 +72,15 @@ def test_select_host_validation(lib):
     assert call(sink=3, recent=2) == -1 and "top_pages" in _err(lib)
     assert call(sink=2 ** 31 - 1, recent=2 ** 31 - 1) == -1
     assert call(Hq=34) == -2 and call(D=64) == -2
-    assert call(maxp=393217) == -2 and "393216" in _err(lib)
-    assert call(maxp=1 << 28) == -2 and call(B=1 << 28) == -2
+    assert call(maxp=1 << 28) == -2 and call(B=1 << 30) == -2
+    assert call(pages=1 << 30) == -2 and "2^31" in _err(lib)
+    need = lib.pfkv_select_pages_workspace_size(2, 2, 9000)
+    assert need >= 2 * 2 * 9000 * 4
+    assert call(wsb=need - 1) == -5 and "too small" in _err(lib)
+    assert call(ws=None) == -1 and call(ws=_fake(0x10080)) == -1
+    assert lib.pfkv_select_pages_workspace_size(2, 0, 8) == 0
+    assert lib.pfkv_select_pages_workspace_size(0, 2, 8) >= 0
+    assert lib.pfkv_select_pages_workspace_size(64, 8, 1 << 20) >= 64 * 8 * (4 << 20)
     assert call(B=0) == 0
     assert call(sel=None) == -1 and "null" in _err(lib)
     assert call(q=_fake(0x10008)) == -1 and call(ks=_fake(0x10001)) == -1 and call(st=_fake(0x10002)) == -1
