@@ -19,19 +19,20 @@
 // Two stages.  Scores: a warp takes some tens of consecutive pages of one
 // (request, KV head), makes the 8-bit query for itself, and reads the 256 bytes
 // of a page's bounds with half a warp (dp4a, two steps of eight pages in flight
-// per half).  Scores are kept as order-preserving 32-bit keys, 1/64 of the bytes
-// read, beside each warp's smallest and largest.
-// List: one CTA per (request, KV head) finds the K-th largest key and writes the
+// per half).  Scores are kept in fp32, 1/64 of the bytes read, beside each warp's
+// smallest and largest; +inf stands for a page that is listed whatever its score
+// and -inf for one outside the pool.
+// List: one CTA per (request, KV head) finds the K-th largest score and writes the
 // list.  A histogram over 256 equal parts of the scores' range says which part
-// holds it; that part's keys, usually few, are compared with one another, or,
-// where scores repeat, counted by their digits, 8 bits a round.  (Parts of the
-// range spread the shared-memory atomics; a float's leading digits would put most
-// keys into a few bins.)  Pages above the threshold, and the lowest-numbered ones
+// holds it; that part's scores, usually few, are compared with one another, or,
+// where scores repeat, counted by the digits of an order-preserving key, 8 bits a
+// round.  (Parts of the range spread the shared-memory atomics; a float's leading
+// digits would put most scores into a few bins.)  Pages above the threshold, and the lowest-numbered ones
 // equal to it, are written in order from prefix sums.
 //
 // Few short lists run both stages in one launch: a cluster of 8 CTAs per list
 // scores into its first CTA's shared memory, and that CTA lists.  Otherwise two
-// kernels with the keys in the workspace: the first is spread evenly over all SMs
+// kernels with the scores in the workspace: the first is spread evenly over all SMs
 // with neighbouring warps on neighbouring heads, so that a page's bounds are read
 // as one run, and the second is resident and waiting when the first ends.
 #include <cuda_bf16.h>
@@ -53,14 +54,13 @@ constexpr int kStep = 2 * kBatch;         // pages per warp and step
 constexpr int kBins = 256;
 constexpr int kMaxListThreads = 1024;
 constexpr int kCluster = 8;                // CTAs of a list in one launch
-constexpr int kFusedPages = 8192;          // keys that such a list may have: 32 KB of shared memory
-constexpr int kCandidates = 512;         // keys compared with one another instead of by digits
-constexpr uint32_t kAlways = 0xFFFFFFFFu;  // key of a page that is listed whatever its score
-constexpr uint32_t kLowest = 0u;           // key of a page outside the pool
+constexpr int kFusedPages = 8192;          // pages that such a list may have: 32 KB of shared memory
+constexpr int kCandidates = 512;           // scores compared with one another instead of by digits
 
-// What a warp of the first kernel leaves beside its keys.
+// What a warp leaves beside its scores: the smallest and largest of those that
+// are not set by rule.
 struct __align__(16) Extent {
-  float low, high;  // of the scores
+  float low, high;
   int32_t bits;     // errors met
   int32_t unused;
 };
@@ -68,7 +68,7 @@ struct __align__(16) Extent {
 struct SelectArgs {
   int32_t* selected;  // [B][Hkv][K]
   int32_t* status;    // [B][Hkv] or null
-  uint32_t* keys;     // [B * Hkv][stride]
+  float* scores;      // [B * Hkv][stride]
   Extent* extents;    // [B * Hkv][chunks]
   const uint16_t* q;
   const int8_t* bounds;
@@ -81,11 +81,12 @@ struct SelectArgs {
   int64_t num_pages, stride;
 };
 
+// A whole number that grows with x.
 __device__ __forceinline__ uint32_t order_key(float x) {
-  const uint32_t u = __float_as_uint(x + 0.f);  // -0 (an underflow) counts as 0
+  const uint32_t u = __float_as_uint(x);
   return u ^ ((u & 0x80000000u) ? 0xFFFFFFFFu : 0x80000000u);
 }
-__device__ __forceinline__ float unordered(uint32_t key) {
+__device__ __forceinline__ float of_order_key(uint32_t key) {
   return __uint_as_float((key & 0x80000000u) ? key ^ 0x80000000u : ~key);
 }
 
@@ -131,14 +132,14 @@ struct ScoreShared {
 };
 
 // The pages first .. first + 8 chunk - 1 of (b, h) by one CTA, chunk to a warp:
-// keys to keys[page] and each warp's extent to extents[page / chunk], in global
+// scores to scores[page] and each warp's extent to extents[page / chunk], in global
 // memory or in a cluster CTA's shared memory; `ready` is called by every thread
 // before the first write.  False, and nothing done, where every page is listed.
 // What does not depend on the length or the query is loaded ahead of them: the
 // chain is block table -> bounds, and the query is made while those arrive.
 template <class Ready>
 __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh, int64_t b, int h, int first,
-                                            int chunk, uint32_t* keys, Extent* extents, Ready ready) {
+                                            int chunk, float* scores, Extent* extents, Ready ready) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int l16 = lane & 15, half = lane >> 4;
   const int own = l16 >> 1;  // the page of the half warp's eight whose sum this lane ends up with
@@ -240,17 +241,17 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
     int sum = ((l16 & 2) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 2) ? s2[0] : s2[1], 2);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
     if (i < count && !(l16 & 1)) {
-      uint32_t key = kLowest;
+      float score = -INFINITY;
       const int index = first + i;
       if (index < a.sink || index >= npages - a.recent) {
-        key = kAlways;
+        score = INFINITY;
       } else if (st.ok) {
         const float x = (float)sum * st.scale;
-        low = fminf(low, x);
-        high = fmaxf(high, x);
-        key = order_key(x);
+        score = x == x ? x + 0.f : -INFINITY;  // NaN (a scale that is none) ranks last, -0 (an underflow) as 0
+        low = fminf(low, score);
+        high = fmaxf(high, score);
       }
-      keys[index] = key;
+      scores[index] = score;
     }
   };
   for (int done = 0; done < count; done += 2 * kStep) {
@@ -280,7 +281,7 @@ __global__ void __launch_bounds__(kScoreWarps * 32, 2) score_pages_kernel(const 
   const int64_t b = br / a.runs, unit = b * a.Hkv + h;
   const int first = run * kScoreWarps * a.chunk;
   if ((int64_t)first * a.P >= a.context_lens[b]) return;
-  score_block(a, sh, b, h, first, a.chunk, a.keys + unit * a.stride, a.extents + unit * a.chunks, [] {});
+  score_block(a, sh, b, h, first, a.chunk, a.scores + unit * a.stride, a.extents + unit * a.chunks, [] {});
 }
 
 // --------------------------------------------------------------------- lists
@@ -302,7 +303,7 @@ __device__ __forceinline__ uint32_t suffix_sum(uint32_t x, uint32_t* red) {
 
 struct ListShared {
   uint32_t hist[5][kBins];  // of parts of the range, then of four digits
-  uint2 cand[kCandidates];  // keys of the part, and which warp's they are
+  float2 cand[kCandidates];  // scores of the part, and which warp's they are
   uint32_t above[kMaxListThreads / 32], equal[kMaxListThreads / 32];  // listed keys of each warp's piece
   float range[2][kMaxListThreads / 32];
   uint32_t bins[kBins / 32];
@@ -316,11 +317,11 @@ __device__ __forceinline__ void list_all(const SelectArgs& a, int64_t unit, int 
   if (a.status && threadIdx.x == 0) a.status[unit] = bits;
 }
 
-// One CTA: the list of `unit` from its npages > K keys (16-byte aligned) and the
+// One CTA: the list of `unit` from its npages > K scores (16-byte aligned) and the
 // nchunks extents of their scores; `ready` is called before they are read.
 template <class Ready>
 __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, int64_t unit, int npages,
-                                          const uint32_t* keys, const Extent* extents, int nchunks, int bits,
+                                          const float* scores, const Extent* extents, int nchunks, int bits,
                                           Ready ready) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int threads = blockDim.x, warps = threads >> 5;
@@ -331,15 +332,18 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
     sh.found[3] = 0;
     sh.err = 0;
   }
-  // keys: each warp a contiguous piece, 128 at a time, four to a lane
+  // scores: each warp a contiguous piece, 128 at a time, four to a lane
   const int piece = ((npages + warps - 1) / warps + 127) & ~127;
   const int p0 = min(warp * piece, npages), p1 = min(p0 + piece, npages);
-  // fn(first index, four keys, how many of them there are); whole warps
+  // fn(first index, four scores, how many indices are left); whole warps
   auto each = [&](auto&& fn) {
 #pragma unroll 1
     for (int i = p0 + 4 * lane; i - 4 * lane < p1; i += 128) {
-      const int n = max(min(p1 - i, 4), 0);
-      fn(i, n > 0 ? *reinterpret_cast<const uint4*>(keys + i) : make_uint4(0u, 0u, 0u, 0u), n);
+      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
+      const int n = p1 - i;
+      if (n > 0) x = *reinterpret_cast<const float4*>(scores + i);
+      const float v[4] = {x.x, x.y, x.z, x.w};
+      fn(i, v, n);
     }
   };
   ready();
@@ -367,17 +371,15 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   // K-th largest; equal scores, or a range that is no number: one part
   float per = (float)kBins / (high - low);
   if (!(high > low) || !isfinite(per)) per = 0.f;
-  auto part_of = [&](uint32_t key) {
-    if (key == kAlways) return kBins - 1;
-    return min(max(__float2int_rd((unordered(key) - low) * per), 0), kBins - 1);  // grows with the key; NaN: 0
+  auto part_of = [&](float x) {  // grows with x; +inf: the last, or 0 if there is one part
+    return min(max(__float2int_rd((x - low) * per), 0), kBins - 1);
   };
-  each([&](int, const uint4& k, int n) {
-    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+  each([&](int, const float (&x)[4], int n) {
 #pragma unroll
     for (int c = 0; c < 4; ++c)
-      if (c < n) atomicAdd(&sh.hist[0][part_of(w[c])], 1u);
+      if (c < n) atomicAdd(&sh.hist[0][part_of(x[c])], 1u);
   });
-  uint32_t want = (uint32_t)a.K;  // of the keys of the part, how many are listed
+  uint32_t want = (uint32_t)a.K;  // of the scores of the part, how many are listed
   // the bin that holds the want-th largest, by the block's first 256 threads
   auto find = [&](const uint32_t* bins) {
     __syncthreads();
@@ -395,77 +397,68 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   const int part = (int)sh.found[0];
   const uint32_t in_part = sh.found[2];
 
-  // ---------------- the threshold: listed are the keys of higher parts, those
-  // of the part with (key & mask) > edge, and the first `want` with == edge;
-  // sh.above and sh.equal count the former and the latter in each warp's piece
-  uint32_t edge = 0, mask = 0xFFFFFFFFu;
+  // ---------------- the threshold: listed are the scores above edge and the
+  // first `want` equal to it; sh.above and sh.equal count both in each warp's piece
+  float edge = 0.f;
   if (in_part <= kCandidates) {  // few: compared with one another
     uint32_t above = 0;
-    each([&](int, const uint4& k, int n) {
-      const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+    each([&](int, const float (&x)[4], int n) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (c < n) {
-          const int at = part_of(w[c]);
+          const int at = part_of(x[c]);
           above += at > part;
-          if (at == part) sh.cand[atomicAdd(&sh.found[3], 1u)] = make_uint2(w[c], (uint32_t)warp);
+          if (at == part) sh.cand[atomicAdd(&sh.found[3], 1u)] = make_float2(x[c], __int_as_float(warp));
         }
     });
     above = __reduce_add_sync(0xFFFFFFFFu, above);
     if (lane == 0) sh.above[warp] = above;
     __syncthreads();
     for (uint32_t i = tid; i < in_part; i += threads) {
-      const uint32_t k = sh.cand[i].x;
+      const float x = sh.cand[i].x;
       uint32_t gt = 0, eq = 0;
+#pragma unroll 4
       for (uint32_t j = 0; j < in_part; ++j) {
-        const uint32_t o = sh.cand[j].x;
-        gt += o > k;
-        eq += o == k;
+        const float o = sh.cand[j].x;
+        gt += o > x;
+        eq += o == x;
       }
+      const int w = __float_as_int(sh.cand[i].y);
       if (gt + eq < want) {  // above the want-th largest
-        atomicAdd(&sh.above[sh.cand[i].y], 1u);
+        atomicAdd(&sh.above[w], 1u);
       } else if (gt < want) {  // equal to it: all of these write the same
-        atomicAdd(&sh.equal[sh.cand[i].y], 1u);
-        sh.found[0] = k;
+        atomicAdd(&sh.equal[w], 1u);
+        sh.found[0] = __float_as_uint(x);
         sh.found[4] = want - gt;
       }
     }
     __syncthreads();
-    edge = sh.found[0];
+    edge = __uint_as_float(sh.found[0]);
     want = sh.found[4];
-  } else {  // many, as where scores repeat: by their digits of 8 bits
-    mask = 0;
+  } else {  // many, as where scores repeat: by the digits of their keys
+    uint32_t key = 0, mask = 0;
 #pragma unroll 1
     for (int p = 1; p <= 4; ++p) {
       const int shift = 32 - 8 * p;
-      each([&](int, const uint4& k, int n) {
-        const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+      each([&](int, const float (&x)[4], int n) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c)
-          if (c < n && (w[c] & mask) == edge && part_of(w[c]) == part)
-            atomicAdd(&sh.hist[p][(w[c] >> shift) & 255], 1u);
+        for (int c = 0; c < 4; ++c) {
+          const uint32_t k = order_key(x[c]);
+          if (c < n && (k & mask) == key && part_of(x[c]) == part) atomicAdd(&sh.hist[p][(k >> shift) & 255], 1u);
+        }
       });
       find(sh.hist[p]);
-      edge |= sh.found[0] << shift;
+      key |= sh.found[0] << shift;
       mask |= 255u << shift;
-      if (sh.found[2] == want) break;  // all of them are listed
     }
-  }
-  // 2: above the threshold, 1: equal to it, 0: below
-  auto place = [&](uint32_t k) {
-    const int at = part_of(k);
-    if (at != part) return at > part ? 2 : 0;
-    return (k & mask) > edge ? 2 : ((k & mask) == edge ? 1 : 0);
-  };
-  if (in_part > kCandidates) {
+    edge = of_order_key(key);
     uint32_t above = 0, equal = 0;
-    each([&](int, const uint4& k, int n) {
-      const uint32_t w[4] = {k.x, k.y, k.z, k.w};
+    each([&](int, const float (&x)[4], int n) {
 #pragma unroll
       for (int c = 0; c < 4; ++c)
         if (c < n) {
-          above += place(w[c]) == 2;
-          equal += place(w[c]) == 1;
+          above += x[c] > edge;
+          equal += x[c] == edge;
         }
     });
     above = __reduce_add_sync(0xFFFFFFFFu, above);
@@ -480,26 +473,31 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   // ---------------- the list, in order
   uint32_t above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.above[lane] : 0u);  // in earlier warps' pieces
   uint32_t equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.equal[lane] : 0u);
-  const uint32_t below = (1u << lane) - 1;
-  each([&](int i, const uint4& k, int n) {
-    const uint32_t w[4] = {k.x, k.y, k.z, k.w};
-    int c[4];
-    uint32_t a2 = above, e2 = equal;  // before this lane's four
+  each([&](int i, const float (&x)[4], int n) {
+    // this lane's two counts in one word, then those of the lanes before it
+    uint32_t mine = 0;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      c[u] = u < n ? place(w[u]) : 0;
-      const uint32_t m2 = __ballot_sync(0xFFFFFFFFu, c[u] == 2), m1 = __ballot_sync(0xFFFFFFFFu, c[u] == 1);
-      a2 += __popc(m2 & below);
-      e2 += __popc(m1 & below);
-      above += __popc(m2);
-      equal += __popc(m1);
-    }
+    for (int c = 0; c < 4; ++c)
+      if (c < n) mine += x[c] > edge ? 0x10000u : (x[c] == edge ? 1u : 0u);
+    if (!__any_sync(0xFFFFFFFFu, mine)) return;
+    uint32_t sum = mine;
 #pragma unroll
-    for (int u = 0; u < 4; ++u) {
-      if (c[u] == 2 || (c[u] == 1 && e2 < want)) out[a2 + min(e2, want)] = i + u;
-      a2 += c[u] == 2;
-      e2 += c[u] == 1;
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+      if (lane >= o) sum += y;
     }
+    const uint32_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+    uint32_t a2 = above + ((sum - mine) >> 16), e2 = equal + ((sum - mine) & 0xFFFFu);
+#pragma unroll
+    for (int c = 0; c < 4; ++c)
+      if (c < n) {
+        const bool gt = x[c] > edge, eq = x[c] == edge;
+        if (gt || (eq && e2 < want)) out[a2 + min(e2, want)] = i + c;
+        a2 += gt;
+        e2 += eq;
+      }
+    above += all >> 16;
+    equal += all & 0xFFFFu;
   });
   if (a.status && tid == 0) a.status[unit] = (int32_t)sh.err;
 }
@@ -514,7 +512,7 @@ __global__ void __launch_bounds__(kMaxListThreads, 1) list_pages_kernel(const Se
     list_all(a, unit, npages, bits);
     return;
   }
-  list_unit(a, sh, unit, npages, a.keys + unit * a.stride, a.extents + unit * a.chunks,
+  list_unit(a, sh, unit, npages, a.scores + unit * a.stride, a.extents + unit * a.chunks,
             (npages + a.chunk - 1) / a.chunk, bits, [] { grid_dependency_wait(); });  // the scores are visible
 }
 
@@ -523,7 +521,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps *
     select_pages_kernel(const SelectArgs a) {
   __shared__ ListShared sh;
   __shared__ ScoreShared ssh;
-  __shared__ __align__(16) uint32_t keys[kFusedPages];
+  __shared__ __align__(16) float scores[kFusedPages];
   __shared__ Extent extents[kCluster * kScoreWarps];
   const int rank = (int)tc::cluster_ctarank();
   const int64_t unit = blockIdx.x / kCluster, b = unit / a.Hkv;
@@ -538,14 +536,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps *
   const int chunk = (per + kStep - 1) / kStep * kStep;
   cluster_arrive();  // this CTA is running: its shared memory may be written
   // the first CTA's arrays, as this CTA sees them
-  score_block(a, ssh, b, (int)(unit % a.Hkv), rank * kScoreWarps * chunk, chunk, map_to_first(keys),
+  score_block(a, ssh, b, (int)(unit % a.Hkv), rank * kScoreWarps * chunk, chunk, map_to_first(scores),
               map_to_first(extents), [] { cluster_wait(); });
   cluster_arrive();
   if (rank != 0) {
     cluster_wait();
     return;
   }
-  list_unit(a, sh, unit, npages, keys, extents, (npages + chunk - 1) / chunk, bits, [] { cluster_wait(); });
+  list_unit(a, sh, unit, npages, scores, extents, (npages + chunk - 1) / chunk, bits, [] { cluster_wait(); });
 }
 
 // One launch while all its clusters are resident at once.
@@ -563,7 +561,7 @@ int pages_per_warp(int64_t pairs, int sms) {
 }
 
 size_t align_up(size_t x) { return (x + 255) / 256 * 256; }
-size_t keys_bytes(int64_t units, int64_t stride) { return align_up((size_t)units * (size_t)stride * 4); }
+size_t scores_bytes(int64_t units, int64_t stride) { return align_up((size_t)units * (size_t)stride * 4); }
 int64_t stride_of(int max_pages) { return ((int64_t)max_pages + 63) / 64 * 64; }
 
 }  // namespace
@@ -574,7 +572,7 @@ extern "C" size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, 
   const int64_t units = (int64_t)batch * num_kv_heads;
   if (pfkv::one_launch(units, max_pages_per_seq, pfkv::device_sm_count())) return 0;
   const int64_t chunks = ((int64_t)max_pages_per_seq + pfkv::kStep - 1) / pfkv::kStep;
-  return pfkv::keys_bytes(units, pfkv::stride_of(max_pages_per_seq)) +
+  return pfkv::scores_bytes(units, pfkv::stride_of(max_pages_per_seq)) +
          pfkv::align_up((size_t)units * (size_t)chunks * sizeof(pfkv::Extent)) + 256;
 }
 
@@ -616,8 +614,8 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   a.selected = selected;
   a.status = unit_status;
   a.stride = stride_of(max_pages_per_seq);
-  a.keys = static_cast<uint32_t*>(workspace);
-  a.extents = reinterpret_cast<Extent*>(static_cast<uint8_t*>(workspace) + keys_bytes(units, a.stride));
+  a.scores = static_cast<float*>(workspace);
+  a.extents = reinterpret_cast<Extent*>(static_cast<uint8_t*>(workspace) + scores_bytes(units, a.stride));
   a.q = static_cast<const uint16_t*>(q);
   a.bounds = bounds;
   a.bound_scales = bound_scales;
