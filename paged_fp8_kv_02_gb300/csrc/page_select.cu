@@ -18,7 +18,7 @@
 //
 // Two stages.  Scores: a warp takes some tens of consecutive pages of one
 // (request, KV head), makes the 8-bit query for itself, and reads the 256 bytes
-// of a page's bounds with half a warp (dp4a, two steps of eight pages in flight
+// of a page's bounds with half a warp (dp4a, two steps of four pages in flight
 // per half).  Scores are kept in fp32, 1/64 of the bytes read, beside each warp's
 // smallest and largest; +inf stands for a page that is listed whatever its score
 // and -inf for one outside the pool.
@@ -49,7 +49,7 @@ namespace {
 constexpr int kD = 128;
 constexpr int kMaxG = 16;
 constexpr int kScoreWarps = 8;
-constexpr int kBatch = 8;                 // pages per half warp and step
+constexpr int kBatch = 4;                 // pages per half warp and step
 constexpr int kStep = 2 * kBatch;         // pages per warp and step
 constexpr int kBins = 256;
 constexpr int kMaxListThreads = 1024;
@@ -142,7 +142,7 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
                                             int chunk, float* scores, Extent* extents, Ready ready) {
   const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
   const int l16 = lane & 15, half = lane >> 4;
-  const int own = l16 >> 1;  // the page of the half warp's eight whose sum this lane ends up with
+  const int own = l16 >> 2;  // the page of the half warp's four whose sum this lane ends up with
   first += warp * chunk;
   const int32_t* table = a.block_tables + b * a.max_pages + first;
   const int room = min(chunk, a.max_pages - first);
@@ -176,7 +176,7 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
     if (a.k_scales) st.scale *= __ldg(a.k_scales + at);
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int pu = __shfl_sync(0xFFFFFFFFu, at, 2 * u, 16);
+      const int pu = __shfl_sync(0xFFFFFFFFu, at, 4 * u, 16);
       st.v[u] = __ldg(reinterpret_cast<const uint4*>(a.bounds) + (int64_t)pu * (2 * kD / 16) + l16);
     }
   };
@@ -229,18 +229,16 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
       s[u] = __dp4a((int)st.v[u].x, (int)qv.x,
                     __dp4a((int)st.v[u].y, (int)qv.y,
                            __dp4a((int)st.v[u].z, (int)qv.z, __dp4a((int)st.v[u].w, (int)qv.w, 0))));
-    // sums over the 16 lanes, each step halving the pages a lane holds: page
-    // `own` ends in lanes 2 own and 2 own + 1
-    int s4[4], s2[2];
-#pragma unroll
-    for (int u = 0; u < 4; ++u)
-      s4[u] = ((l16 & 8) ? s[u + 4] : s[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 8) ? s[u] : s[u + 4], 8);
+    // sums over the 16 lanes, two steps halving the pages a lane holds: page
+    // `own` ends in lanes 4 own .. 4 own + 3
+    int s2[2];
 #pragma unroll
     for (int u = 0; u < 2; ++u)
-      s2[u] = ((l16 & 4) ? s4[u + 2] : s4[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 4) ? s4[u] : s4[u + 2], 4);
-    int sum = ((l16 & 2) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 2) ? s2[0] : s2[1], 2);
+      s2[u] = ((l16 & 8) ? s[u + 2] : s[u]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 8) ? s[u] : s[u + 2], 8);
+    int sum = ((l16 & 4) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 4) ? s2[0] : s2[1], 4);
+    sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
-    if (i < count && !(l16 & 1)) {
+    if (i < count && !(l16 & 3)) {
       float score = -INFINITY;
       const int index = first + i;
       if (index < a.sink || index >= npages - a.recent) {
@@ -272,7 +270,7 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
   return true;
 }
 
-__global__ void __launch_bounds__(kScoreWarps * 32, 2) score_pages_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 4) score_pages_kernel(const SelectArgs a) {
   __shared__ ScoreShared sh;
   grid_launch_dependents();  // the listing kernel may take its place and wait
   const int h = (int)(blockIdx.x % a.Hkv);  // neighbouring CTAs: neighbouring heads of the same pages
@@ -551,12 +549,16 @@ bool one_launch(int64_t units, int max_pages, int sms) {
   return max_pages <= kFusedPages && units * kCluster <= 2 * (int64_t)sms;
 }
 
-// Pages per warp of the first kernel: about four warps a scheduler on every SM,
-// and at least the step that a warp takes at once.
+// Pages per warp of the first kernel: about 32 warps on every SM if all lists were
+// as long as the table, at least the step that a warp takes at once, at most 64:
+// lists shorter than the table then still spread (64 requests of up to 2K pages,
+// 16 to 256 pages a warp: 28.9, 24.8, 22.0, 28.0, 43.9 us; 8 of 4K-16K pages: 57.0,
+// 47.0, 43.3, 42.4, 55.2).  Eight pages a step with two CTAs per SM instead of four
+// with four: 24.4 and 42.1 us at their best.
 int pages_per_warp(int64_t pairs, int sms) {
-  const int64_t even = pairs / ((int64_t)sms * 24);
+  const int64_t even = pairs / ((int64_t)sms * 32);
   int c = kStep;
-  while (c < 256 && c < even) c *= 2;
+  while (c < 64 && c < even) c *= 2;
   return c;
 }
 
