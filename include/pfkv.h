@@ -301,10 +301,14 @@ PFKV_API int pfkv_paged_decode_attn_noalloc(void *out, const void *q, const void
  * that largest scale grows, as for the running maximum of the softmax).
  * Per block: two loads per 16-token tile, each K scale on the tile's raw
  * scores, V scales as weights as per token; 8 / page_size extra bytes per row.
- * Numerics: per tensor, per head and per block as pfkv_paged_decode_attn; per token, the
+ * Numerics: per tensor and per head as pfkv_paged_decode_attn; per token and
+ * per block, the
  * score products are f16 on K widened in registers, against q times one
  * power of two per work unit that takes its largest |q| into (2^14, 2^15]
  * (any finite bf16 q; exact for every value at least 2^-29 of that largest).
+ * Per block with kv_split_tokens = 0, tables of few tokens are taken by the
+ * kernel of pfkv_paged_sparse_decode_attn (the status word in the workspace is
+ * written all the same).
  * Scales: finite and >= 0 (TENSOR, HEAD: > 0); not checked (device arrays).
  * The scale of a token past L_b is never used.  Workspace: as
  * pfkv_paged_decode_attn (pfkv_paged_decode_workspace_size).  Other arguments

@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
 #pragma unroll
       for (int i = 0; i < 16; ++i) qf[j][i >> 1][i & 1] = wd[i];  // bf16 pairs
     }
-    if constexpr (!kBf16 && kScl == kSclToken) {
+    if constexpr (!kBf16 && (kScl == kSclToken || kScl == kSclBlock)) {
       // Q in f16 for the widened-K products, times a power of two s over the
       // unit's heads taking max |q s| into (2^14, 2^15]: every finite bf16
       // query fits and each value at least 2^-29 of the largest is an exact
@@ -619,9 +619,10 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
                      qf[j][ks][1]);
         }
       }
-    } else if constexpr (kScl == kSclToken) {
+    } else if constexpr (kScl == kSclToken || kScl == kSclBlock) {
       // per-token scales: K widened to f16 (this variant is at its register
-      // limit, where the e4m3 products' Q parts cost more than they save)
+      // limit, where the e4m3 products' Q parts cost more than they save);
+      // per block too (8 x 32K-256K tokens 327.8 -> 322.3 us)
       const uint4 x0 = lds128(kb + swz(g, 2 * t)), x1 = lds128(kb + swz(g, 2 * t + 1));
       const uint4 y0 = lds128(kb + swz(g + 8, 2 * t)), y1 = lds128(kb + swz(g + 8, 2 * t + 1));
       const uint32_t xr[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w};
@@ -650,21 +651,22 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
                    qf[j][2 * kk + 1][1]);
         }
       }
-      // undo the Q scale (a power of two: exact); a tile lies in one page, so
-      // the block's K scale rides along
-      float tile_ks = 1.f;
-      if constexpr (kScl == kSclBlock) tile_ks = sptr[2 * stage];
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        const float f0 = kScl == kSclBlock ? qinv[j][0] * tile_ks : qinv[j][0];
-        const float f1 = kScl == kSclBlock ? qinv[j][1] * tile_ks : qinv[j][1];
-        s[j][0] *= f0;
-        s[j][1] *= f1;
-        s[j][2] *= f0;
-        s[j][3] *= f1;
+      for (int j = 0; j < NT; ++j) {  // undo the Q scale (a power of two: exact)
+        s[j][0] *= qinv[j][0];
+        s[j][1] *= qinv[j][1];
+        s[j][2] *= qinv[j][0];
+        s[j][3] *= qinv[j][1];
       }
     }
 
+    if constexpr (kScl == kSclBlock) {  // a tile lies in one page
+      const float ks = sptr[2 * stage] * qinv[0][0];
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) s[j][i] *= ks;
+    }
     // ---------------- per-token scales: this thread's tokens are g and g + 8
     float ks0 = 1.f, ks8 = 1.f, vs0 = 0.f, vs8 = 0.f;
     if constexpr (kScl == kSclToken) {
@@ -1260,6 +1262,14 @@ size_t pfkv_paged_decode_workspace_size(int batch, int num_q_heads, int num_kv_h
 namespace pfkv {
 namespace {
 
+// Whether tables of so many tokens, for so many (request, KV head) pairs, are taken
+// by the kernel without a plan, a merge and their launches: one cluster of up to 64
+// warps per pair, even over the pairs and not over the tokens.  us there and here:
+// 8 pairs of 1K / 4K / 8K / 32K tokens 10.3 / 12.3 / 14.4 / 32.8 and 28.3 / 83.3 / 60.7 /
+// 68.5; 512 of up to 1K / 2K / 4K / 8K 22.6 / 36.9 / 62.4 / 105.8 and 25.9 / 35.8 / 52.7 /
+// 74.0; 64 of 8K / up to 32K 29.4 / 65.6 and 38.4 / 55.8; 1536 of up to 2K 80.7 and 77.6.
+bool short_blocks(int64_t pairs, int64_t tokens) { return tokens <= 32768 && pairs * tokens <= (int64_t)1 << 20; }
+
 // The decode entry for every scale mode: kSclHost takes k_scale / v_scale;
 // kSclUnit, kSclToken and kSclBlock read the device arrays k_scales / v_scales (unit
 // mode: one scale per KV head when head_stride is 1, one for all when 0).
@@ -1343,6 +1353,11 @@ int decode_entry(void* out, const void* q, const void* k_cache, const void* v_ca
     a.score_scale = a.logit_scale;
     a.out_scale = 1.f;
   }
+
+  if (scl == kSclBlock && kv_split_tokens == 0 && short_blocks((int64_t)batch * num_kv_heads, (int64_t)max_pages_per_seq * page_size))
+    return decode_short_blocks(out, q, k_cache, v_cache, k_scales, v_scales, block_tables, max_pages_per_seq,
+                               context_lens, batch, num_q_heads, num_kv_heads, page_size, num_pages, softmax_scale,
+                               a.status, lse_out, reinterpret_cast<cudaStream_t>(stream));
 
   const bool bf16 = cache_dtype == PFKV_CACHE_BF16;
   const cuuint64_t rows = (cuuint64_t)num_pages * num_kv_heads * page_size;

@@ -35,4 +35,13 @@ int encode_tensor_map(CUtensorMap* map, CUtensorMapDataType dtype, cuuint32_t ra
                       const cuuint64_t* dims, const cuuint64_t* strides_bytes,
                       const cuuint32_t* box, CUtensorMapSwizzle swizzle);
 
+// Dense decode with scales per block over tables of few pages: the sparse
+// kernel with every page listed (sparse_decode.cu).  Arguments are checked by the
+// caller; *status_word is zeroed and receives the device errors.
+int decode_short_blocks(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables, int max_pages_per_seq,
+                        const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads, int page_size,
+                        int64_t num_pages, float softmax_scale, int32_t* status_word, float* lse_out,
+                        cudaStream_t stream);
+
 }  // namespace pfkv

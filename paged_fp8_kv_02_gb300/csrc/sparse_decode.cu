@@ -51,11 +51,12 @@ struct SparseArgs {
   const uint16_t* q;
   const float* k_scales;
   const float* v_scales;
-  const int32_t* selected;  // [B][Hkv][K]
+  const int32_t* selected;  // [B][Hkv][K], or null: all pages in order
   const int32_t* block_tables;
   const int32_t* context_lens;
   float* lse;
-  int32_t* status;  // [B][Hkv] or null
+  int32_t* status;       // [B][Hkv] or null
+  int32_t* status_word;  // one for the call, zeroed before, or null
   int Hq, Hkv, G, P, max_pages, K;
   int64_t num_pages;
   int page_stride, head_stride;  // scale index = page * page_stride + head * head_stride
@@ -81,13 +82,13 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
   const uint32_t wbase = smem_base + warp * kWarpBytes;
   uint8_t* const wptr = smem_raw + (smem_base - smem_u32(smem_raw)) + warp * kWarpBytes;
   const uint32_t bar0 = smem_u32(&bars[warp][0]);
-  const int32_t* const list = a.selected + unit * a.K;
+  const int32_t* const list = a.selected ? a.selected + unit * a.K : nullptr;
   const int tpp = a.P / kTile;  // tiles per page
   const int nw = nc * kWarps, gw = rank * kWarps + warp;
   // what does not depend on the length: the warp's first entries if the list is
   // as long as it may be, and the queries
   const int guess = (int)((uint32_t)(gw * a.K * tpp) / nw / tpp);  // a list has fewer than 2^26 tiles, nw <= 32
-  const int guessed = __ldg(list + min(guess + lane, a.K - 1));
+  const int guessed = list ? __ldg(list + min(guess + lane, a.K - 1)) : guess + lane;
   uint4 qrow[NT][4];
   tile::load_q<NT>(a.q + ((int64_t)b * a.Hq + (int64_t)h * a.G) * kD, a.G, lane, qrow);
 
@@ -123,7 +124,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     tokens = 0;
     const int slot = s0 + lane;
     if (slot * tpp >= f_end) return;
-    const int logical = s0 == guess ? guessed : __ldg(list + slot);
+    const int logical = s0 == guess ? guessed : (list ? __ldg(list + slot) : slot);
     if (logical < 0) return;  // padding
     if (logical >= npages) {
       bits |= kErrBadTopk;
@@ -132,11 +133,12 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     page = __ldg(a.block_tables + (int64_t)b * a.max_pages + logical);
     if (page < 0 || (int64_t)page >= a.num_pages) {
       bits |= kErrBadPage;
-      return;
+      if (list) return;  // a list passes it over
+      page = -1;         // dense decode reads zeros: boxes outside the tensor, zero scales
     }
     const int64_t si = (int64_t)page * a.page_stride + h * a.head_stride;
-    ks = __ldg(a.k_scales + si);
-    vs = __ldg(a.v_scales + si);
+    ks = page >= 0 ? __ldg(a.k_scales + si) : 0.f;
+    vs = page >= 0 ? __ldg(a.v_scales + si) : 0.f;
     tokens = min(a.P, L - logical * a.P);
   };
   auto look_up = [&](int s0) {
@@ -414,6 +416,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     for (int r = 0; r < nc; ++r) all |= tc::ld_cluster_u32(tc::mapa(smem_u32(&err), r));
     a.status[unit] = (int32_t)all;
   }
+  if (a.status_word && threadIdx.x == 0 && err) atomicOr(a.status_word, (int32_t)err);
   __syncwarp();
   tc::cluster_sync();  // no CTA leaves while another may still read its shared memory
 }
@@ -456,7 +459,58 @@ int launch(const CUtensorMap& tmK, const CUtensorMap& tmV, const SparseArgs& a, 
   return check_cuda("paged_sparse_decode launch");
 }
 
+int launch_for(const SparseArgs& a, const void* k_cache, const void* v_cache, int64_t units, cudaStream_t stream) {
+  const cuuint64_t dims[2] = {kD, (cuuint64_t)a.num_pages * a.Hkv * a.P};
+  const cuuint64_t strides[1] = {kD};
+  const cuuint32_t box[2] = {kD, (cuuint32_t)kTile};
+  CUtensorMap tmK, tmV;
+  int rc = encode_tensor_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(k_cache), dims, strides, box,
+                             CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc == PFKV_OK)
+    rc = encode_tensor_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(v_cache), dims, strides, box,
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+  if (rc != PFKV_OK) return rc;
+  // lists of up to a quarter of the SMs' number: eight warps a CTA (1 / 2 / 4 requests
+  // of the lists above 11.4 / 15.3 / 16.8 us instead of 15.4 / 17.7 / 18.2 with four, 8
+  // requests 27.3 instead of 26.6)
+  const bool wide = units * 4 <= device_sm_count();
+  if (a.G <= 8) return wide ? launch<1, 8>(tmK, tmV, a, units, stream) : launch<1, 4>(tmK, tmV, a, units, stream);
+  return wide ? launch<2, 8>(tmK, tmV, a, units, stream) : launch<2, 4>(tmK, tmV, a, units, stream);
+}
+
 }  // namespace
+
+int decode_short_blocks(void* out, const void* q, const void* k_cache, const void* v_cache, const float* k_scales,
+                        const float* v_scales, const int32_t* block_tables, int max_pages_per_seq,
+                        const int32_t* context_lens, int batch, int num_q_heads, int num_kv_heads, int page_size,
+                        int64_t num_pages, float softmax_scale, int32_t* status_word, float* lse_out,
+                        cudaStream_t stream) {
+  if (cudaMemsetAsync(status_word, 0, sizeof(int32_t), stream) != cudaSuccess)
+    return check_cuda("paged_decode status reset");
+  SparseArgs a;
+  a.out = static_cast<uint16_t*>(out);
+  a.q = static_cast<const uint16_t*>(q);
+  a.k_scales = k_scales;
+  a.v_scales = v_scales;
+  a.selected = nullptr;
+  a.block_tables = block_tables;
+  a.context_lens = context_lens;
+  a.lse = lse_out;
+  a.status = nullptr;
+  a.status_word = status_word;
+  a.Hq = num_q_heads;
+  a.Hkv = num_kv_heads;
+  a.G = num_q_heads / num_kv_heads;
+  a.P = page_size;
+  a.max_pages = max_pages_per_seq;
+  a.K = max_pages_per_seq;
+  a.num_pages = num_pages;
+  a.page_stride = num_kv_heads;
+  a.head_stride = 1;
+  a.logit_scale = softmax_scale * kLog2e;
+  return launch_for(a, k_cache, v_cache, (int64_t)batch * num_kv_heads, stream);
+}
+
 }  // namespace pfkv
 
 extern "C" int pfkv_paged_sparse_decode_attn(void* out, const void* q, const void* k_cache, const void* v_cache,
@@ -519,6 +573,7 @@ extern "C" int pfkv_paged_sparse_decode_attn(void* out, const void* q, const voi
   a.context_lens = context_lens;
   a.lse = lse_out;
   a.status = unit_status;
+  a.status_word = nullptr;
   a.Hq = num_q_heads;
   a.Hkv = num_kv_heads;
   a.G = G;
@@ -529,21 +584,5 @@ extern "C" int pfkv_paged_sparse_decode_attn(void* out, const void* q, const voi
   a.page_stride = page_stride;
   a.head_stride = head_stride;
   a.logit_scale = softmax_scale * kLog2e;
-  const cuuint64_t dims[2] = {kD, (cuuint64_t)num_pages * num_kv_heads * page_size};
-  const cuuint64_t strides[1] = {kD};
-  const cuuint32_t box[2] = {kD, (cuuint32_t)kTile};
-  CUtensorMap tmK, tmV;
-  int rc = encode_tensor_map(&tmK, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(k_cache), dims, strides, box,
-                             CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc == PFKV_OK)
-    rc = encode_tensor_map(&tmV, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void*>(v_cache), dims, strides, box,
-                           CU_TENSOR_MAP_SWIZZLE_128B);
-  if (rc != PFKV_OK) return rc;
-  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
-  // lists of up to a quarter of the SMs' number: eight warps a CTA (1 / 2 / 4 requests
-  // of the lists above 11.4 / 15.3 / 16.8 us instead of 15.4 / 17.7 / 18.2 with four, 8
-  // requests 27.3 instead of 26.6)
-  const bool wide = units * 4 <= device_sm_count();
-  if (G <= 8) return wide ? launch<1, 8>(tmK, tmV, a, units, s) : launch<1, 4>(tmK, tmV, a, units, s);
-  return wide ? launch<2, 8>(tmK, tmV, a, units, s) : launch<2, 4>(tmK, tmV, a, units, s);
+  return launch_for(a, k_cache, v_cache, units, reinterpret_cast<cudaStream_t>(stream));
 }

@@ -227,9 +227,10 @@ def check_rows(out, lse, q, sets, softmax_scale, what=""):
             assert excess <= 1, (what, "lse", b, h, excess)
 
 
-def run_decode(p, rng, lens, Hq, Hkv, P, split=0, spread=4):
+def run_decode(p, rng, lens, Hq, Hkv, P, split=0, spread=4, width=0):
     import torch
     bt, c = filled(rng, lens, Hkv, P, spread)
+    bt = np.pad(bt, ((0, 0), (0, max(0, width - bt.shape[1]))), constant_values=-1)
     q, qv = bf16(rng.standard_normal((len(lens), Hq, 128)) * np.exp2(rng.integers(-3, 2, (len(lens), Hq, 1))))
     out = Guarded(q.shape, torch.bfloat16, "cuda")
     lse = Guarded(q.shape[:2], torch.float32, "cuda")
@@ -253,15 +254,24 @@ def test_block_decode_matches_reference(Hq, Hkv, P, lens, split):
     run_decode(pf(), np.random.default_rng(Hq + P), list(lens), Hq, Hkv, P, split)
 
 
-def test_block_decode_scales_over_many_binades():
-    run_decode(pf(), np.random.default_rng(1), [700, 1300], 16, 2, 16, 0, spread=20)
+@pytest.mark.parametrize("width", [0, 4096])
+def test_block_decode_scales_over_many_binades(width):
+    run_decode(pf(), np.random.default_rng(1), [700, 1300], 16, 2, 16, 0, spread=20, width=width)
 
 
-def test_block_decode_bad_page_reads_zeros():
+@pytest.mark.parametrize("Hq,Hkv,P,lens", [(8, 2, 16, (1, 0, 17, 3000)), (16, 1, 64, (1300, 64)), (48, 48, 16, (200,))])
+def test_block_decode_by_table_width(Hq, Hkv, P, lens):
+    """Narrow tables take one kernel, wide ones another: both at their borders."""
+    for tokens in (0, 32768, 32784, (1 << 20) // (len(lens) * Hkv), (1 << 20) // (len(lens) * Hkv) + P):
+        run_decode(pf(), np.random.default_rng(tokens), list(lens), Hq, Hkv, P, width=tokens // P)
+
+
+@pytest.mark.parametrize("width", [3, 4096])
+def test_block_decode_bad_page_reads_zeros(width):
     import torch
     p, rng, P = pf(), np.random.default_rng(2), 16
     bt, c = filled(rng, [40, 40], 1, P)
-    bad = bt.copy()
+    bad = np.pad(bt, ((0, 0), (0, width - 3)), constant_values=-1)
     bad[0, 0], bad[1, 1] = -5, c["k"].shape[0] + 7
     q, qv = bf16(rng.standard_normal((2, 4, 128)))
     out = torch.empty_like(q)
