@@ -955,8 +955,9 @@ constexpr int kMergeLoads = 4;              // segments per warp whose loads are
 
 // kMergeHeads query heads of one (request, KV head) per CTA; calls with
 // explicit chunks use 1 (many small CTAs), calls without them use
-// merge_unsplit_kernel below.
-template <int kMergeHeads>
+// merge_unsplit_kernel below.  kSpread: a unit without explicit chunks is folded
+// by all warps too, instead of by one.
+template <int kMergeHeads, bool kSpread>
 __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const DecodeArgs a) {
   __shared__ float4 red_o[kMergeWarps][kMergeHeads][32];
   __shared__ float red_m[kMergeWarps][kMergeHeads], red_l[kMergeWarps][kMergeHeads];
@@ -985,7 +986,7 @@ __global__ void __launch_bounds__(kMergeThreads) merge_kernel(const DecodeArgs a
   const int64_t ts = a.tile_start[b] + (int64_t)kvh * ntiles;
   const int64_t u0 = a.unit_start[b] + (int64_t)kvh * nchunks;
   if (nchunks == 1 && owner_of(ts, W, N) == owner_of(ts + ntiles - 1, W, N)) return;  // direct
-  if (nchunks == 1) {
+  if (nchunks == 1 && !kSpread) {
     // one warp per head (with one head per CTA, warp 0)
     const int e = g_lo + (kMergeHeads == 1 ? 0 : warp);
     if ((kMergeHeads == 1 && warp != 0) || e >= g_hi) return;
@@ -1231,7 +1232,12 @@ int launch_decode(const CUtensorMap& tmK, const CUtensorMap& tmV, const DecodeAr
   cudaError_t e;
   if (a.chunk_tiles < (1 << 30)) {
     cfg.gridDim = dim3(a.B * a.Hq);
-    e = cudaLaunchKernelEx(&cfg, merge_kernel<1>, args);
+    e = cudaLaunchKernelEx(&cfg, merge_kernel<1, false>, args);
+  } else if (kScl == kSclBlock && args.nwarps >= (int64_t)16 * a.B * a.Hkv) {
+    // each unit was covered by 16 warps or more: eight warps fold a head's
+    // states instead of one (8 x 32K-256K tokens, 38 states a head: 314 -> 305 us)
+    cfg.gridDim = dim3(a.B * a.Hq);
+    e = cudaLaunchKernelEx(&cfg, merge_kernel<1, true>, args);
   } else {
     cfg.gridDim = dim3((unsigned)(((int64_t)a.B * a.Hq + kMergeWarps - 1) / kMergeWarps));
     e = cudaLaunchKernelEx(&cfg, merge_unsplit_kernel, args);
