@@ -70,9 +70,13 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
 // kHold 16-element pieces of the page's new rows in registers between the
 // maximum and the conversion (the launch gives the block enough threads that
 // all of them fit for the page sizes up to 64; larger pages read the rest again).
+// The rows' place does not depend on the page, so they are on their way while the
+// block table and the old scale are read.  kChunks: 16-element pieces of a row, or
+// 0 where it is not known beforehand.
 constexpr int kHold = 4;
 constexpr int kMaxThreads = 512;
 
+template <int kChunks>
 __global__ void __launch_bounds__(kMaxThreads) kv_append_block_kernel(const BlockAppendArgs a) {
   __shared__ float warp_max[kMaxThreads / 32];
   const int which = blockIdx.y;
@@ -85,19 +89,13 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_block_kernel(const Bloc
   const int t0 = L - n;               // position of the first new token
   const int logical = t0 / a.P + i;
   if ((int64_t)logical * a.P >= L) return;
-  const int page = a.block_tables[(int64_t)b * a.max_pages + logical];
-  if (page < 0 || (int64_t)page >= a.num_pages) return;  // skipped; validate_tables reports
   const int base = logical * a.P;
   const int lo = max(t0 - base, 0), hi = min(L - base, a.P);  // the page's new rows
-  const int chunks = a.D >> 4;
-  const int64_t sidx = (int64_t)page * a.H + h;
-  float* const scale = (which ? a.scale[1] : a.scale[0]) + sidx;
-  uint8_t* const dst = (which ? a.cache[1] : a.cache[0]) + sidx * a.P * a.D;
+  const int chunks = kChunks ? kChunks : a.D >> 4;
   const uint16_t* const src =
       (which ? a.x[1] : a.x[0]) + ((int64_t)(s0 + base + lo - t0) * a.H + h) * a.D;
   const int64_t row_stride = (int64_t)a.H * a.D;
   const int pieces = (hi - lo) * chunks;
-  const float old = lo > 0 ? *scale : 0.f;
 
   uint4 x0[kHold], x1[kHold];
   float m = 0.f;
@@ -111,6 +109,12 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_block_kernel(const Bloc
       x1[k] = __ldcs(p + 1);
     }
   }
+  const int page = a.block_tables[(int64_t)b * a.max_pages + logical];
+  if (page < 0 || (int64_t)page >= a.num_pages) return;  // skipped; validate_tables reports
+  const int64_t sidx = (int64_t)page * a.H + h;
+  float* const scale = (which ? a.scale[1] : a.scale[0]) + sidx;
+  uint8_t* const dst = (which ? a.cache[1] : a.cache[0]) + sidx * a.P * a.D;
+  const float old = lo > 0 ? *scale : 0.f;
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
     if (threadIdx.x + k * blockDim.x < pieces) m = fmaxf(m, amax16(x0[k], x1[k]));
@@ -212,7 +216,11 @@ extern "C" int pfkv_kv_append_fp8_block(const void* k_new, const void* v_new, vo
   const int64_t rows = a.max_new < page_size ? a.max_new : page_size;
   int64_t threads = (rows * (head_dim / 16) + kHold * 32 - 1) / (kHold * 32) * 32;
   if (threads > kMaxThreads) threads = kMaxThreads;
-  kv_append_block_kernel<<<dim3((unsigned)blocks, has_v ? 2 : 1), (unsigned)threads, 0,
-                           reinterpret_cast<cudaStream_t>(stream)>>>(a);
+  const dim3 grid((unsigned)blocks, has_v ? 2 : 1);
+  cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
+  if (head_dim == 128)
+    kv_append_block_kernel<8><<<grid, (unsigned)threads, 0, s>>>(a);
+  else
+    kv_append_block_kernel<0><<<grid, (unsigned)threads, 0, s>>>(a);
   return check_cuda("kv_append_fp8_block launch");
 }
