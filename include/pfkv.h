@@ -386,7 +386,8 @@ PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const voi
  *                 bytes (query it on the device that will run the call),
  *                 256-byte aligned; contents on entry are ignored.  It holds the
  *                 scores, 4 bytes per KV head and block-table entry; 0 bytes and
- *                 NULL where few short lists keep them on the SMs.
+ *                 NULL where few short lists keep them on the SMs.  Calls that
+ *                 may overlap on the GPU need one each.
  * Supported: head_dim 128; G in 1..16; sink_pages + recent_pages <= top_pages;
  * num_pages * num_kv_heads < 2^31; any page_size. */
 PFKV_API size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq);

@@ -114,7 +114,9 @@ __global__ void __launch_bounds__(kMaxThreads) kv_append_block_kernel(const Bloc
   const int64_t sidx = (int64_t)page * a.H + h;
   float* const scale = (which ? a.scale[1] : a.scale[0]) + sidx;
   uint8_t* const dst = (which ? a.cache[1] : a.cache[0]) + sidx * a.P * a.D;
-  const float old = lo > 0 ? *scale : 0.f;
+  // a stored scale that is none (never written) counts as 0
+  const float stored = lo > 0 ? *scale : 0.f;
+  const float old = stored > 0.f ? stored : 0.f;
 #pragma unroll
   for (int k = 0; k < kHold; ++k)
     if (threadIdx.x + k * blockDim.x < pieces) m = fmaxf(m, amax16(x0[k], x1[k]));

@@ -87,7 +87,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
   const int nw = nc * kWarps, gw = rank * kWarps + warp;
   // what does not depend on the length: the warp's first entries if the list is
   // as long as it may be, and the queries
-  const int guess = (int)((uint32_t)(gw * a.K * tpp) / nw / tpp);  // a list has fewer than 2^26 tiles, nw <= 32
+  const int guess = (int)((uint32_t)gw * (uint32_t)(a.K * tpp) / nw / tpp);  // a list has fewer than 2^26 tiles, nw <= 64
   const int guessed = list ? __ldg(list + min(guess + lane, a.K - 1)) : guess + lane;
   uint4 qrow[NT][4];
   tile::load_q<NT>(a.q + ((int64_t)b * a.Hq + (int64_t)h * a.G) * kD, a.G, lane, qrow);

@@ -131,6 +131,28 @@ def test_append_scale_at_its_borders(amax):
     st.check(f"amax {amax}")
 
 
+@pytest.mark.parametrize("bad", [np.nan, -1.0, 0.0])
+def test_append_over_a_scale_that_is_none(bad):
+    """Earlier rows whose scale was never written become zeros; the new rows
+    and their scale are as on a fresh page."""
+    import torch
+    st = State(9, [20], 2, 128, 16)
+    st.s["k"].t.fill_(bad)
+    k, kv = bf16(st.rng.standard_normal((3, 2, 128)))
+    pf().kv_append_fp8_block(k, None, st.g["k"].t, None, st.s["k"].t, None, dev(st.bt), dev(np.array([11], np.int32)),
+                             dev(np.array([0, 3], np.int32)), 3)
+    torch.cuda.synchronize()
+    got, sc = st.g["k"].t.cpu().numpy(), st.s["k"].t.cpu().numpy()
+    page = int(st.bt[0, 0])
+    for h in range(2):
+        s = ref.block_scale(float(np.abs(kv[:, h]).max()))
+        assert sc[page, h] == s
+        assert np.array_equal(got[page, h, 8:11], ref.encode(kv[:, h] / s))
+        codes = st.ref["k"][page, h, :8]
+        fine = (codes & 0x7F) != 0x7F
+        assert np.all((got[page, h, :8] & 0x7F)[fine] == 0)
+
+
 def test_append_leaves_out_what_does_not_fit():
     """Requests with impossible numbers and pages outside the pool are skipped,
     the others written; nothing else changes."""

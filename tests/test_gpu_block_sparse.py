@@ -128,6 +128,49 @@ def test_select_queries_of_any_size(qscale):
     run_select([4000], 8, 1, 16, 40, 0, 0, qscale=qscale)
 
 
+def test_select_by_two_kernels_in_a_graph_and_on_two_streams():
+    """The path with a workspace: replayed from a graph with new queries, and
+    two calls at once with a workspace each."""
+    import torch
+    p, rng, P, top = pf(), np.random.default_rng(17), 1, 100
+    lens = [9000, 8500, 50]
+    bt, pages = tables(rng, lens, P)
+    bnd, bs = random_bounds(rng, pages, 2)
+    q = [bf16(rng.standard_normal((3, 8, 128))) for _ in range(3)]
+    d = [dev(bnd), dev(bs), dev(bt), dev(np.array(lens, np.int32))]
+    assert p.select_pages_workspace_size(3, 2, bt.shape[1]) > 0
+    sel = [torch.empty((3, 2, top), dtype=torch.int32, device="cuda") for _ in range(2)]
+    ws = [torch.empty(p.select_pages_workspace_size(3, 2, bt.shape[1]), dtype=torch.uint8, device="cuda") for _ in range(2)]
+    qin = q[0][0].clone()
+    call = lambda i, x: p.select_pages(sel[i], x, *d, P, 1, 2, workspace=ws[i])
+    call(0, qin)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call(0, qin)
+    for x, xv in q:
+        qin.copy_(x)
+        graph.replay()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert np.array_equal(sel[0].cpu().numpy(), ref.select(xv, bnd, bs, None, bt, lens, P, top, 1, 2))
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    for _ in range(5):
+        for i, s in enumerate(streams):
+            with torch.cuda.stream(s):
+                call(i, q[i][0])
+    torch.cuda.synchronize()
+    for i in range(2):
+        assert np.array_equal(sel[i].cpu().numpy(), ref.select(q[i][1], bnd, bs, None, bt, lens, P, top, 1, 2))
+    # a stream argument, the workspace left to the call
+    sel[0].fill_(-5)
+    torch.cuda.synchronize()
+    for _ in range(3):
+        p.select_pages(sel[0], q[1][0], *d, P, 1, 2, stream=streams[0])
+    streams[0].synchronize()
+    assert np.array_equal(sel[0].cpu().numpy(), ref.select(q[1][1], bnd, bs, None, bt, lens, P, top, 1, 2))
+
+
 def test_select_bad_pages_and_lengths():
     import torch
     p, rng, P, top = pf(), np.random.default_rng(9), 16, 4
