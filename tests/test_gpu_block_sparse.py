@@ -419,3 +419,52 @@ def test_refusals_of_tensors_that_do_not_match():
         with pytest.raises(ValueError):
             p.page_key_bounds(**{**good, name: t})
     torch.cuda.synchronize()
+
+
+def test_offsets_beyond_31_bits():
+    """Pages at the far end of caches of 2.9 GB each: the same results as the
+    same rows in a small pool."""
+    import torch
+    p, rng, H, P, pages = pf(), np.random.default_rng(23), 8, 64, 45000
+    lens = [700, 65]
+    n = [-(-m // P) for m in lens]
+    small = {x: np.zeros((sum(n), H, P, 128), np.uint8) for x in "kv"}
+    scales = {x: np.zeros((sum(n), H), np.float32) for x in "kv"}
+    sbt = np.full((2, max(n)), -1, np.int32)
+    sbt[0, :n[0]], sbt[1, :n[1]] = np.arange(n[0]), n[0] + np.arange(n[1])
+    bt = np.where(sbt >= 0, pages - 1 - sbt, -1).astype(np.int32)
+    start = np.array([0, 700, 765], np.int32)
+    big = {x: torch.empty((pages, H, P, 128), dtype=torch.uint8, device="cuda") for x in "kv"}
+    bsc = {x: torch.empty((pages, H), device="cuda") for x in "kv"}
+    new = {x: bf16(rng.standard_normal((765, H, 128))) for x in "kv"}
+    ctx = dev(np.array(lens, np.int32))
+    p.kv_append_fp8_block(new["k"][0], new["v"][0], big["k"], big["v"], bsc["k"], bsc["v"], dev(bt), ctx, dev(start), 700)
+    torch.cuda.synchronize()
+    for x in "kv":
+        ref.append(new[x][1], small[x], scales[x], sbt, lens, start, 700)
+        for b in range(2):
+            for i in range(n[b]):
+                hi = min(P, lens[b] - i * P)
+                got = big[x][int(bt[b, i])].cpu().numpy()
+                assert np.array_equal(got[:, :hi], small[x][sbt[b, i], :, :hi])
+                assert np.array_equal(bsc[x][int(bt[b, i])].cpu().numpy(), scales[x][sbt[b, i]])
+    bnd, bs = torch.empty((pages, H, 2, 128), dtype=torch.int8, device="cuda"), torch.empty((pages, H), device="cuda")
+    rb, rs = np.zeros((sum(n), H, 2, 128), np.int8), np.zeros((sum(n), H), np.float32)
+    p.page_key_bounds(bnd, bs, big["k"], dev(bt), ctx, dev(start), 700)
+    ref.bounds(small["k"], rb, rs, sbt, lens, start, 700)
+    q, qv = bf16(rng.standard_normal((2, 64, 128)))
+    sel = torch.empty((2, H, 4), dtype=torch.int32, device="cuda")
+    p.select_pages(sel, q, bnd, bs, dev(bt), ctx, P, 1, 1, k_scales=bsc["k"])
+    want = ref.select(qv, rb, rs, scales["k"], sbt, lens, P, 4, 1, 1)
+    assert np.array_equal(sel.cpu().numpy(), want)
+    out, lse = torch.empty_like(q), torch.empty((2, 64), device="cuda")
+    c = {"k": small["k"], "v": small["v"], "ks": scales["k"], "vs": scales["v"]}
+    cache = (big["k"], big["v"], p.SCALE_BLOCK, bsc["k"], bsc["v"])
+    p.paged_sparse_decode_attn(out, q, *cache, sel, dev(bt), ctx, 0.088, lse_out=lse)
+    sets = [[subset(c, sbt[b], h, m, P, want[b, h][want[b, h] >= 0]) for h in range(H)] for b, m in enumerate(lens)]
+    check_rows(out.double().cpu().numpy(), lse.cpu().numpy(), qv, sets, 0.088)
+    for split in (0, 64):
+        p.paged_decode_attn_scaled(out, q, *cache, dev(bt), ctx, 0.088, kv_split_tokens=split, lse_out=lse,
+                                   max_total_chunks=13)
+        sets = [[context(c, sbt[b], h, m, P) for h in range(H)] for b, m in enumerate(lens)]
+        check_rows(out.double().cpu().numpy(), lse.cpu().numpy(), qv, sets, 0.088)
