@@ -334,14 +334,18 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   const int piece = ((npages + warps - 1) / warps + 127) & ~127;
   const int p0 = min(warp * piece, npages), p1 = min(p0 + piece, npages);
   // fn(first index, four scores, how many indices are left); whole warps
+  auto piece_at = [&](int i) {
+    return i < p1 ? *reinterpret_cast<const float4*>(scores + i) : make_float4(0.f, 0.f, 0.f, 0.f);
+  };
   auto each = [&](auto&& fn) {
+    int i = p0 + 4 * lane;
+    float4 next = piece_at(i);
 #pragma unroll 1
-    for (int i = p0 + 4 * lane; i - 4 * lane < p1; i += 128) {
-      float4 x = make_float4(-INFINITY, -INFINITY, -INFINITY, -INFINITY);
-      const int n = p1 - i;
-      if (n > 0) x = *reinterpret_cast<const float4*>(scores + i);
+    for (; i - 4 * lane < p1; i += 128) {
+      const float4 x = next;
+      next = piece_at(i + 128);  // on its way while x is looked at
       const float v[4] = {x.x, x.y, x.z, x.w};
-      fn(i, v, n);
+      fn(i, v, p1 - i);
     }
   };
   ready();
