@@ -405,8 +405,8 @@ PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *b
  *   granularity   PFKV_SCALE_TENSOR, _HEAD or _BLOCK (per token: unsupported)
  *   selected      int32 [batch][num_kv_heads][top_pages], logical pages, each at
  *                 most once, in any order; entries < 0 are padding.  Only the
- *                 first ceil(L_b / page_size) entries are read: a list of
- *                 distinct pages has no more.  An entry beyond the context is
+ *                 first ceil(L_b / page_size) entries count: a list of distinct
+ *                 pages has no more.  An entry beyond the context is
  *                 passed over (PFKV_DEVERR_BAD_TOPK), as is a page outside the
  *                 pool (PFKV_DEVERR_BAD_PAGE).
  *   lse_out       optional fp32 [batch][num_q_heads]
