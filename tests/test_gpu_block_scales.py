@@ -270,7 +270,8 @@ def run_decode(p, rng, lens, Hq, Hkv, P, split=0, spread=4, width=0):
 
 @pytest.mark.parametrize("Hq,Hkv,P,lens", [
     (8, 2, 16, (1, 16, 17, 300)), (16, 1, 64, (0, 130, 64, 5)), (4, 4, 48, (33, 96, 47, 100)), (20, 4, 128, (1000, 3)),
-    (64, 8, 16, (2049, 257, 1, 31, 512)), (7, 1, 96, (5000,))])
+    (64, 8, 16, (2049, 257, 1, 31, 512)), (7, 1, 96, (5000,)), (32, 2, 16, tuple(range(0, 1200, 57))),
+    (30, 15, 16, tuple(range(0, 900, 45)))])
 @pytest.mark.parametrize("split", [0, 64])
 def test_block_decode_matches_reference(Hq, Hkv, P, lens, split):
     run_decode(pf(), np.random.default_rng(Hq + P), list(lens), Hq, Hkv, P, split)

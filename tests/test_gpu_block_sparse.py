@@ -222,7 +222,10 @@ def subset(c, bt_row, h, L, P, pages):
 @pytest.mark.parametrize("Hq,Hkv,P,top,lens", [
     (8, 2, 16, 4, (1, 16, 17, 300, 0)), (16, 1, 64, 40, (5000, 64, 63)), (4, 4, 48, 1, (33, 96, 500)),
     (20, 4, 128, 9, (1000, 3, 129)), (64, 8, 16, 128, (2049, 257, 1, 31, 512, 6000)), (7, 1, 96, 33, (5000, 9000)),
-    (48, 48, 16, 20, (700,)), (8, 1, 16, 1000, (16000, 15999, 40))])
+    (48, 48, 16, 20, (700,)), (8, 1, 16, 1000, (16000, 15999, 40)),
+    (32, 2, 16, 30, tuple(range(1, 1200, 57))),   # 42 lists of 16 heads
+    (18, 6, 32, 25, tuple(range(3, 2000, 117))),  # 108 lists: clusters of 3 or 4
+    (30, 15, 16, 12, tuple(range(1, 900, 45)))])  # 300 lists: clusters of 1 or 2
 @pytest.mark.parametrize("gran", [0, 1, 3])
 def test_sparse_decode_matches_reference(Hq, Hkv, P, top, lens, gran):
     import torch
