@@ -19,7 +19,7 @@
 // Two stages.  Scores: a warp takes some tens of consecutive pages of one
 // (request, KV head), makes the 8-bit query for itself, and reads the 256 bytes
 // of a page's bounds with half a warp (dp4a, two steps of four pages in flight
-// per half).  Scores are kept in fp32, 1/64 of the bytes read, beside each warp's
+// per half; table entries and scales for 32 pages at a time, a group ahead).  Scores are kept in fp32, 1/64 of the bytes read, beside each warp's
 // smallest and largest; +inf stands for a page that is listed whatever its score
 // and -inf for one outside the pool.
 // List: one CTA per (request, KV head) finds the K-th largest score and writes the
@@ -59,7 +59,7 @@ constexpr int kStep = 2 * kBatch;         // pages per warp and step
 constexpr int kBins = 256;
 constexpr int kMaxListThreads = 1024;
 constexpr int kCluster = 8;                // CTAs of a list in one launch
-constexpr int kFusedPages = 8192;          // pages that such a list may have: 32 KB of shared memory
+constexpr int kFusedPages = 2048;          // pages that such a list may have
 constexpr int kCandidates = 512;           // scores compared with one another instead of by digits
 
 // What a warp leaves beside its scores: the smallest and largest of those that
@@ -151,10 +151,10 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
   first += warp * chunk;
   const int32_t* table = a.block_tables + b * a.max_pages + first;
   const int room = min(chunk, a.max_pages - first);
-  auto entry = [&](int i) { return i < room ? __ldg(table + i) : -1; };
-  int i = half * kBatch + own;
-  const int page0 = entry(i);
-  int next = entry(i + kStep);
+  // the table's entries of 32 pages, one per lane
+  auto entries = [&](int g) { return 32 * g + lane < room ? __ldg(table + 32 * g + lane) : -1; };
+  const int pages0 = entries(0);
+  int pages_next = entries(1);
   // thread d < 128: channel d of the group's rows
   uint32_t row[kMaxG];
   {
@@ -167,26 +167,39 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
   if (npages <= a.K) return false;
   const int count = max(min(chunk, npages - first), 0);
 
+  float low = INFINITY, high = -INFINITY;
+  // the lane's page of a group: its place in the bounds and its scale, in two parts
+  // so that nothing waits for them here
+  struct Group {
+    int at;
+    float bs, ks;
+  };
+  auto look_up = [&](int g, int page) {
+    Group x{0, NAN, 1.f};  // entry 0 stands in for one that is not there; its score is no number
+    const bool ok = page >= 0 && (int64_t)page < a.num_pages;
+    if (32 * g + lane < count && !ok) bits |= kErrBadPage;
+    if (ok) {
+      x.at = page * a.Hkv + h;
+      x.bs = __ldg(a.bound_scales + x.at);
+      if (a.k_scales) x.ks = __ldg(a.k_scales + x.at);
+    }
+    return x;
+  };
   struct Step {
     uint4 v[kBatch];
-    float scale;
-    bool ok;
   };
-  float low = INFINITY, high = -INFINITY;
-  auto load = [&](Step& st, int i, int page) {
-    st.ok = page >= 0 && (int64_t)page < a.num_pages;
-    if (i < count && !st.ok) bits |= kErrBadPage;
-    const int at = st.ok ? page * a.Hkv + h : 0;  // entry 0 stands in for one that is not there
-    st.scale = __ldg(a.bound_scales + at);
-    if (a.k_scales) st.scale *= __ldg(a.k_scales + at);
+  // bounds of pages 8 s .. 8 s + 7 of a group; read once by one warp: they leave L1
+  // and L2 first, and the scales and tables beside them stay
+  auto load = [&](Step& st, const Group& x, int g, int s) {
 #pragma unroll
     for (int u = 0; u < kBatch; ++u) {
-      const int pu = __shfl_sync(0xFFFFFFFFu, at, 4 * u, 16);
-      st.v[u] = __ldg(reinterpret_cast<const uint4*>(a.bounds) + (int64_t)pu * (2 * kD / 16) + l16);
+      const int pu = __shfl_sync(0xFFFFFFFFu, x.at, kStep * s + kBatch * half + u);
+      st.v[u] = __ldcs(reinterpret_cast<const uint4*>(a.bounds) + (int64_t)pu * (2 * kD / 16) + l16);
     }
   };
+  Group cur = look_up(0, pages0);
   Step x, y;
-  load(x, i, page0);
+  load(x, cur, 0, 0);
 
   // ---------------- the group's query in 8-bit whole numbers
   uint32_t largest = 0;
@@ -227,7 +240,7 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
   if (count == 0) return true;
 
   // ---------------- the warp's pages, two steps of loads in flight
-  auto sum_up = [&](const Step& st, int i) {
+  auto sum_up = [&](const Step& st, float group_scale, int g, int step) {
     int s[kBatch];
 #pragma unroll
     for (int u = 0; u < kBatch; ++u)
@@ -243,30 +256,36 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
     int sum = ((l16 & 4) ? s2[1] : s2[0]) + __shfl_xor_sync(0xFFFFFFFFu, (l16 & 4) ? s2[0] : s2[1], 4);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 2);
     sum += __shfl_xor_sync(0xFFFFFFFFu, sum, 1);
+    const int mine = kStep * step + kBatch * half + own, i = 32 * g + mine;
+    const float scale = __shfl_sync(0xFFFFFFFFu, group_scale, mine);
     if (i < count && !(l16 & 3)) {
-      float score = -INFINITY;
       const int index = first + i;
+      float score = (float)sum * scale + 0.f;  // + 0: -0 (an underflow) counts as 0
       if (index < a.sink || index >= npages - a.recent) {
         score = INFINITY;
-      } else if (st.ok) {
-        const float x = (float)sum * st.scale;
-        score = x == x ? x + 0.f : -INFINITY;  // NaN (a scale that is none) ranks last, -0 (an underflow) as 0
+      } else if (score != score) {
+        score = -INFINITY;  // a page outside the pool, a scale that is none
+      } else {
         low = fminf(low, score);
         high = fmaxf(high, score);
       }
       scores[index] = score;
     }
   };
-  for (int done = 0; done < count; done += 2 * kStep) {
-    int page = next;
-    next = entry(i + 2 * kStep);
-    load(y, i + kStep, page);
-    sum_up(x, i);
-    page = next;
-    next = entry(i + 3 * kStep);
-    load(x, i + 2 * kStep, page);
-    sum_up(y, i + kStep);
-    i += 2 * kStep;
+#pragma unroll 1
+  for (int g = 0; 32 * g < count; ++g) {
+    const Group nxt = look_up(g + 1, pages_next);
+    pages_next = entries(g + 2);
+    const float scale = cur.bs * cur.ks;
+    load(y, cur, g, 1);
+    sum_up(x, scale, g, 0);
+    load(x, cur, g, 2);
+    sum_up(y, scale, g, 1);
+    load(y, cur, g, 3);
+    sum_up(x, scale, g, 2);
+    load(x, nxt, g + 1, 0);
+    sum_up(y, scale, g, 3);
+    cur = nxt;
   }
   low = warp_min(low);
   high = -warp_min(-high);
@@ -553,17 +572,22 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps *
   list_unit(a, sh, unit, npages, scores, extents, (npages + chunk - 1) / chunk, bits, [] { cluster_wait(); });
 }
 
-// One launch while all its clusters are resident at once.
+// One launch while all its clusters are resident at once and the pages are few.
+// Device us in one launch and two, and us of a call from Python: 8 lists of 512 pages
+// 6.3 (11.4) and 6.5 (19.8), of 2048 8.5 (10.9) and 8.2 (19.8), of 8192 17.1 (19.1) and
+// 11.8 (19.9); 32 lists of 2048 9.4 (12.6) and 10.5 (19.7), of 8192 29.5 and 22.6; 64 lists
+// of 512 13.0 and 9.7.
 bool one_launch(int64_t units, int max_pages, int sms) {
   return max_pages <= kFusedPages && units * kCluster <= 2 * (int64_t)sms;
 }
 
 // Pages per warp of the first kernel: about 32 warps on every SM if all lists were
 // as long as the table, at least the step that a warp takes at once, at most 64:
-// lists shorter than the table then still spread (64 requests of up to 2K pages,
-// 16 to 256 pages a warp: 28.9, 24.8, 22.0, 28.0, 43.9 us; 8 of 4K-16K pages: 57.0,
-// 47.0, 43.3, 42.4, 55.2).  Eight pages a step with two CTAs per SM instead of four
-// with four: 24.4 and 42.1 us at their best.
+// lists shorter than the table then still spread (64 requests of up to 2K pages, 32
+// to 256 pages a warp: 21.5, 20.5, 23.7, 31.9 us; 8 of 4K-16K pages: 38.6, 37.9, 36.7,
+// 41.6; 8 of 64K pages: 216.8, 209.2, 205.6, 208.1).  Three CTAs per SM instead of four:
+// 23.2, 40.1 and 220.0 us with 64.  Bounds through the ordinary cache policy instead of
+// streaming ones: 21.9, 42.9 and 258.5.
 int pages_per_warp(int64_t pairs, int sms) {
   const int64_t even = pairs / ((int64_t)sms * 32);
   int c = kStep;
@@ -656,10 +680,12 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   if (blocks > 0x7FFFFFFF) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: too many pages");
   score_pages_kernel<<<(unsigned)blocks, kScoreWarps * 32, 0, s>>>(a);
   // the listing kernel is launched as a programmatic dependent: its CTAs wait
-  // (griddepcontrol.wait) for the scores.  A list's threads: as many as its
-  // keys keep busy while all lists are resident together
+  // (griddepcontrol.wait) for the scores.  A list's threads: as many as its pages
+  // keep busy, and as leave every list resident twice over (whole calls with 256 / 512
+  // / 1024: 512 lists of 2K pages 70.5 / 72.9 / 81.7 us, 256 of 1K 21.8 / 21.1 / 25.4, 64 of
+  // 16K 94.7 / 79.2 / 73.0)
   int threads = kBins;
-  while (threads < kMaxListThreads && threads * 4 < max_pages_per_seq && units * 2 * threads <= (int64_t)sms * 2048)
+  while (threads < kMaxListThreads && threads * 4 < max_pages_per_seq && units * 4 * threads <= (int64_t)sms * 2048)
     threads *= 2;
   cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

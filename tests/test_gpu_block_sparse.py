@@ -103,7 +103,7 @@ def test_select_equals_reference(Hq, Hkv, P, top, sink, recent):
 
 def test_select_ties_go_to_the_lower_page():
     run_select([3000, 5001], 8, 2, 16, 100, 0, 0, flat=True)
-    run_select([50000], 8, 1, 16, 1000, 2, 3, flat=True)   # a cluster a list
+    run_select([32000], 8, 1, 16, 1000, 2, 3, flat=True)   # a cluster a list
     run_select([9000, 8999], 8, 1, 1, 1500, 2, 3, flat=True)  # two kernels
     run_select([9000], 8, 1, 1, 8999, 0, 0, flat=True)
     run_select([3000], 8, 2, 16, 17, 0, 1, qbits=np.zeros(128))  # every score is zero
@@ -117,6 +117,8 @@ def test_select_large_tables(top):
     run_select([4096 * 7] * 20, 8, 8, 16, min(top, 1700), 1, 1, seed=3)
     run_select([8192, 8191], 8, 2, 1, top, 1, 1, seed=4)
     run_select([8193, 8191], 8, 2, 1, top, 1, 1, seed=5)
+    run_select([2048, 2047, 300], 8, 2, 1, min(top, 2040), 1, 1, seed=6)
+    run_select([2049, 2047, 300], 8, 2, 1, min(top, 2040), 1, 1, seed=7)
 
 
 def test_select_table_much_wider_than_the_contexts():
