@@ -329,7 +329,7 @@ struct ListShared {
   uint32_t above[kMaxListThreads / 32], equal[kMaxListThreads / 32];  // listed keys of each warp's piece
   float range[2][kMaxListThreads / 32];
   uint32_t bins[kBins / 32];
-  uint32_t found[5];
+  uint32_t found[6];
   uint32_t err;
 };
 
@@ -426,12 +426,16 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   // ---------------- the threshold: listed are the scores above edge and the
   // first `want` equal to it; sh.above and sh.equal count both in each warp's piece
   float edge = 0.f;
+  bool whole = false;  // every score equal to edge is listed
   if (in_part <= kCandidates) {  // few: compared with one another
     uint32_t above = 0;
+    // below every score of the part, by half a part
+    const float floor = part > 0 ? low + ((float)part - 0.5f) / per : -INFINITY;
     each([&](int, const float (&x)[4], int n) {
+      if (fmaxf(fmaxf(x[0], x[1]), fmaxf(x[2], x[3])) < floor) return;  // most, where few pages of many are listed
 #pragma unroll
       for (int c = 0; c < 4; ++c)
-        if (c < n) {
+        if (c < n && x[c] >= floor) {
           const int at = part_of(x[c]);
           above += at > part;
           if (at == part) sh.cand[atomicAdd(&sh.found[3], 1u)] = make_float2(x[c], __int_as_float(warp));
@@ -456,11 +460,13 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
         atomicAdd(&sh.equal[w], 1u);
         sh.found[0] = __float_as_uint(x);
         sh.found[4] = want - gt;
+        sh.found[5] = eq;
       }
     }
     __syncthreads();
     edge = __uint_as_float(sh.found[0]);
     want = sh.found[4];
+    whole = sh.found[5] == want;
   } else {  // many, as where scores repeat: by the digits of their keys
     uint32_t key = 0, mask = 0;
 #pragma unroll 1
@@ -499,32 +505,53 @@ __device__ __forceinline__ void list_unit(const SelectArgs& a, ListShared& sh, i
   // ---------------- the list, in order
   uint32_t above = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.above[lane] : 0u);  // in earlier warps' pieces
   uint32_t equal = __reduce_add_sync(0xFFFFFFFFu, lane < warp ? sh.equal[lane] : 0u);
-  each([&](int i, const float (&x)[4], int n) {
-    // this lane's two counts in one word, then those of the lanes before it
-    uint32_t mine = 0;
+  const uint32_t below = (1u << lane) - 1;
+  if (whole) {
+    uint32_t at = above + equal;
+    each([&](int i, const float (&x)[4], int n) {
+      uint32_t before = at;
+      bool in[4];
 #pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < n) mine += x[c] > edge ? 0x10000u : (x[c] == edge ? 1u : 0u);
-    if (!__any_sync(0xFFFFFFFFu, mine)) return;
-    uint32_t sum = mine;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
-      if (lane >= o) sum += y;
-    }
-    const uint32_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
-    uint32_t a2 = above + ((sum - mine) >> 16), e2 = equal + ((sum - mine) & 0xFFFFu);
-#pragma unroll
-    for (int c = 0; c < 4; ++c)
-      if (c < n) {
-        const bool gt = x[c] > edge, eq = x[c] == edge;
-        if (gt || (eq && e2 < want)) out[a2 + min(e2, want)] = i + c;
-        a2 += gt;
-        e2 += eq;
+      for (int c = 0; c < 4; ++c) {
+        in[c] = c < n && x[c] >= edge;
+        const uint32_t all = __ballot_sync(0xFFFFFFFFu, in[c]);
+        before += __popc(all & below);
+        at += __popc(all);
       }
-    above += all >> 16;
-    equal += all & 0xFFFFu;
-  });
+#pragma unroll
+      for (int c = 0; c < 4; ++c) {
+        if (in[c]) out[before] = i + c;
+        before += in[c];
+      }
+    });
+  } else {
+    each([&](int i, const float (&x)[4], int n) {
+      // this lane's two counts in one word, then those of the lanes before it
+      uint32_t mine = 0;
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) mine += x[c] > edge ? 0x10000u : (x[c] == edge ? 1u : 0u);
+      if (!__any_sync(0xFFFFFFFFu, mine)) return;
+      uint32_t sum = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t y = __shfl_up_sync(0xFFFFFFFFu, sum, o);
+        if (lane >= o) sum += y;
+      }
+      const uint32_t all = __shfl_sync(0xFFFFFFFFu, sum, 31);
+      uint32_t a2 = above + ((sum - mine) >> 16), e2 = equal + ((sum - mine) & 0xFFFFu);
+#pragma unroll
+      for (int c = 0; c < 4; ++c)
+        if (c < n) {
+          const bool gt = x[c] > edge, eq = x[c] == edge;
+          if (gt || (eq && e2 < want)) out[a2 + min(e2, want)] = i + c;
+          a2 += gt;
+          e2 += eq;
+        }
+      above += all >> 16;
+      equal += all & 0xFFFFu;
+    });
+  }
   if (a.status && tid == 0) a.status[unit] = (int32_t)sh.err;
 }
 
