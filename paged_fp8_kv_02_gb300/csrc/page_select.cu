@@ -30,7 +30,7 @@
 // digits would put most scores into a few bins.)  Pages above the threshold, and
 // the lowest-numbered ones equal to it, are written in order from prefix sums.
 //
-// Few short lists run both stages in one launch: a cluster of 8 CTAs per list
+// Few short lists run both stages in one launch: a cluster of 1 to 8 CTAs per list
 // scores into its first CTA's shared memory, and that CTA lists.  Otherwise two
 // kernels with the scores in the workspace: the first is spread evenly over all SMs
 // with neighbouring warps on neighbouring heads, so that a page's bounds are read
@@ -58,7 +58,7 @@ constexpr int kBatch = 4;                 // pages per half warp and step
 constexpr int kStep = 2 * kBatch;         // pages per warp and step
 constexpr int kBins = 256;
 constexpr int kMaxListThreads = 1024;
-constexpr int kCluster = 8;                // CTAs of a list in one launch
+constexpr int kMaxCluster = 8;             // CTAs of a list in one launch
 constexpr int kFusedPages = 2048;          // pages that such a list may have
 constexpr int kCandidates = 512;           // scores compared with one another instead of by digits
 
@@ -570,14 +570,13 @@ __global__ void __launch_bounds__(kMaxListThreads, 1) list_pages_kernel(const Se
 }
 
 // ------------------------------------------------------- both stages at once
-__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps * 32, 2)
-    select_pages_kernel(const SelectArgs a) {
+__global__ void __launch_bounds__(kScoreWarps * 32, 2) select_pages_kernel(const SelectArgs a) {
   __shared__ ListShared sh;
   __shared__ ScoreShared ssh;
   __shared__ __align__(16) float scores[kFusedPages];
-  __shared__ Extent extents[kCluster * kScoreWarps];
-  const int rank = (int)tc::cluster_ctarank();
-  const int64_t unit = blockIdx.x / kCluster, b = unit / a.Hkv;
+  __shared__ Extent extents[kMaxCluster * kScoreWarps];
+  const int nc = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
+  const int64_t unit = blockIdx.x / nc, b = unit / a.Hkv;
   int bits;
   const int npages = pages_of(a, (int)b, &bits);
   if (npages <= a.K) {  // the whole cluster takes this path
@@ -585,7 +584,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps *
     return;
   }
   // even chunks, a multiple of what a warp takes at once
-  const int per = (npages + kCluster * kScoreWarps - 1) / (kCluster * kScoreWarps);
+  const int per = (npages + nc * kScoreWarps - 1) / (nc * kScoreWarps);
   const int chunk = (per + kStep - 1) / kStep * kStep;
   cluster_arrive();  // this CTA is running: its shared memory may be written
   // the first CTA's arrays, as this CTA sees them
@@ -599,13 +598,25 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kScoreWarps *
   list_unit(a, sh, unit, npages, scores, extents, (npages + chunk - 1) / chunk, bits, [] { cluster_wait(); });
 }
 
-// One launch while all its clusters are resident at once and the pages are few.
-// Device us in one launch and two, and us of a call from Python: 8 lists of 512 pages
-// 6.3 (11.4) and 6.5 (19.8), of 2048 8.5 (10.9) and 8.2 (19.8), of 8192 17.1 (19.1) and
-// 11.8 (19.9); 32 lists of 2048 9.4 (12.6) and 10.5 (19.7), of 8192 29.5 and 22.6; 64 lists
-// of 512 13.0 and 9.7.
-bool one_launch(int64_t units, int max_pages, int sms) {
-  return max_pages <= kFusedPages && units * kCluster <= 2 * (int64_t)sms;
+// CTAs per list if scores and list are done in one launch, 0 if by two kernels.  One
+// launch while all its CTAs are resident at once, two to an SM, and the pages are few:
+// no more than 64 for a warp.  Device us (and of a call from Python) by size of the
+// cluster, and by two kernels:
+//   lists x pages      8            4            2            1            two
+//     8 x 2048     7.8 (10.7)   9.2 (11.6)  11.8 (14.6)  17.3 (19.2)   8.3 (23.0)
+//    32 x 1024     7.9 (10.6)   7.5 (10.2)   8.7 (10.8)  11.4 (14.2)  10.8 (21.2)
+//    64 x 512     13.5 (16.7)   7.8 (10.4)   7.5 (10.6)   8.7 (11.0)  10.4 (22.7)
+//    64 x 2048    17.1 (20.4)  12.2 (14.6)  15.3 (18.4)  24.7 (26.8)  12.6 (21.3)
+//   128 x 1024    24.4 (27.1)  16.2 (18.8)  11.6 (14.6)  14.8 (16.9)  12.9 (21.3)
+//   256 x 512     41.4 (43.8)  25.2 (27.1)  16.7 (18.8)  11.8 (14.6)  12.4 (20.5)
+//   256 x 2048    54.8 (57.7)  42.9 (45.6)  36.2 (39.2)  30.4 (33.1)  31.0 (34.2)
+//   512 x 512     78.6 (81.6)  45.3 (47.6)  32.4 (35.1)  23.5 (26.1)  19.0 (22.5)
+// 8 lists of 8192 pages take 17.1 us in one launch of eight and 11.8 in two.
+int one_launch(int64_t units, int max_pages, int sms) {
+  int c = kMaxCluster;
+  while (c > 1 && units * c > 2 * (int64_t)sms) c /= 2;
+  const bool fits = units * c <= 2 * (int64_t)sms && max_pages <= min(kFusedPages, c * kScoreWarps * 64);
+  return fits ? c : 0;
 }
 
 // Pages per warp of the first kernel: about 32 warps on every SM if all lists were
@@ -632,7 +643,7 @@ int64_t stride_of(int max_pages) { return ((int64_t)max_pages + 63) / 64 * 64; }
 extern "C" size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq) {
   if (batch < 0 || num_kv_heads <= 0 || max_pages_per_seq <= 0) return 0;
   const int64_t units = (int64_t)batch * num_kv_heads;
-  if (pfkv::one_launch(units, max_pages_per_seq, pfkv::device_sm_count())) return 0;
+  if (pfkv::one_launch(units, max_pages_per_seq, pfkv::device_sm_count()) > 0) return 0;
   const int64_t chunks = ((int64_t)max_pages_per_seq + pfkv::kStep - 1) / pfkv::kStep;
   return pfkv::scores_bytes(units, pfkv::stride_of(max_pages_per_seq)) +
          pfkv::align_up((size_t)units * (size_t)chunks * sizeof(pfkv::Extent)) + 256;
@@ -696,8 +707,19 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   a.num_pages = num_pages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
-  if (one_launch(units, max_pages_per_seq, sms)) {
-    select_pages_kernel<<<(unsigned)(units * kCluster), kScoreWarps * 32, 0, s>>>(a);
+  cudaLaunchAttribute attr[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = attr;
+  cfg.numAttrs = 1;
+  if (const int c = one_launch(units, max_pages_per_seq, sms); c > 0) {
+    attr[0].id = cudaLaunchAttributeClusterDimension;
+    attr[0].val.clusterDim.x = (unsigned)c;
+    attr[0].val.clusterDim.y = 1;
+    attr[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(units * c));
+    cfg.blockDim = dim3(kScoreWarps * 32);
+    (void)cudaLaunchKernelEx(&cfg, select_pages_kernel, a);
     return check_cuda("select_pages launch");
   }
   a.chunk = pages_per_warp(units * max_pages_per_seq, sms);
@@ -714,15 +736,10 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   int threads = kBins;
   while (threads < kMaxListThreads && threads * 4 < max_pages_per_seq && units * 4 * threads <= (int64_t)sms * 2048)
     threads *= 2;
-  cudaLaunchAttribute attr[1];
   attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   attr[0].val.programmaticStreamSerializationAllowed = 1;
-  cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3((unsigned)units);
   cfg.blockDim = dim3((unsigned)threads);
-  cfg.stream = s;
-  cfg.attrs = attr;
-  cfg.numAttrs = 1;
   if (cudaLaunchKernelEx(&cfg, list_pages_kernel, a) != cudaSuccess) return check_cuda("select_pages launch");
   return check_cuda("select_pages launch");
 }

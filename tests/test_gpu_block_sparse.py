@@ -130,6 +130,15 @@ def test_select_queries_of_any_size(qscale):
     run_select([4000], 8, 1, 16, 40, 0, 0, qscale=qscale)
 
 
+@pytest.mark.parametrize("batch", [9, 10, 13, 19, 20, 38, 39, 76])
+@pytest.mark.parametrize("width", [2, 64, 512, 1024, 2048])
+def test_select_for_every_cluster(batch, width):
+    # 4 lists a request; the cluster of a list and one launch or two follow from both sizes
+    rng = np.random.default_rng(width + batch)
+    lens = [8 * width, 8 * width - 7, 0, 1] + [int(n) for n in rng.integers(0, 8 * width + 1, batch - 4)]
+    run_select(lens, 8, 4, 8, max(1, width // 3), 1, 1 if width > 2 else 0, seed=batch, ks=batch % 2 == 0, width=width)
+
+
 def test_select_by_two_kernels_in_a_graph_and_on_two_streams():
     """The path with a workspace: replayed from a graph with new queries, and
     two calls at once with a workspace each."""
