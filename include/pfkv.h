@@ -348,7 +348,7 @@ PFKV_API int pfkv_paged_decode_attn_scaled(void *out, const void *q, const void 
  *     s = the smallest power of two >= 2^-15 with A <= 127 s
  *     bounds[page][h][0][d] = floor(lo_d / s)
  *     bounds[page][h][1][d] = ceil(hi_d / s),  bound_scales[page][h] = s
- * K codes that are NaN are passed over.
+ * K codes that are NaN are passed over; a channel with no others has bounds 0.
  *   bounds        int8 [num_pages][num_kv_heads][2][head_dim], written
  *   bound_scales  fp32 [num_pages][num_kv_heads], written
  *   k_cache       e4m3 [num_pages][num_kv_heads][page_size][head_dim]

@@ -113,11 +113,23 @@ __global__ void __launch_bounds__(kWarps * 32) page_bounds_kernel(const BoundsAr
     const uint32_t mine = half ? e[k + 4] : e[k];
     f[k] = up ? max_f16x2(mine, got) : min_f16x2(mine, got);
   }
-  float m = 0.f;
+  auto largest = [&]() {  // over the warp
+    float m = 0.f;
 #pragma unroll
-  for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(f16_lo(f[k])), fabsf(f16_hi(f[k]))));
+    for (int k = 0; k < 4; ++k) m = fmaxf(m, fmaxf(fabsf(f16_lo(f[k])), fabsf(f16_hi(f[k]))));
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+    return m;
+  };
+  float m = largest();
+  if (m > 448.f) {  // a channel with NaN codes only still has infinite ends: it counts as 0
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      if (fabsf(f16_lo(f[k])) > 448.f) f[k] &= 0xFFFF0000u;
+      if (fabsf(f16_hi(f[k])) > 448.f) f[k] &= 0x0000FFFFu;
+    }
+    m = largest();
+  }
   // smallest power of two s with m <= 127 s = 1.984375 2^6 s, at least 2^-15
   const uint32_t u = __float_as_uint(m);
   const int ex = max((int)(u >> 23) - 6 + ((u & 0x7FFFFFu) > 0x7E0000u ? 1 : 0), 127 - 15);

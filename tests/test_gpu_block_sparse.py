@@ -63,6 +63,25 @@ def test_bounds_pass_over_nan_codes_and_what_does_not_fit():
     assert np.array_equal(got.cpu().numpy(), want) and np.array_equal(sc.cpu().numpy(), want_s)
 
 
+def test_bounds_of_channels_with_only_nan_codes():
+    import torch
+    p, rng, P = pf(), np.random.default_rng(5), 16
+    lens = np.array([16, 17, 33], np.int32)  # the last pages hold one token
+    bt, pages = tables(rng, lens, P)
+    k = rng.integers(0, 0x70, (pages, 2, P, 128)).astype(np.uint8)
+    zeros = k.copy()  # such a channel counts as 0, and the others as if it were not there
+    for b, i, h, d in ((0, 0, 1, slice(3, 9)), (1, 1, 0, 127), (2, 2, 0, slice(0, 128)), (2, 1, 1, slice(16, 40, 8))):
+        k[bt[b, i], h, :, d] = 0xFF if h else 0x7F
+        zeros[bt[b, i], h, :, d] = 0
+    got, sc = torch.zeros((pages, 2, 2, 128), dtype=torch.int8, device="cuda"), torch.zeros((pages, 2), device="cuda")
+    want, want_s = got.cpu().numpy().copy(), sc.cpu().numpy().copy()
+    start = np.concatenate([[0], np.cumsum(lens)]).astype(np.int32)
+    p.page_key_bounds(got, sc, dev(k), dev(bt), dev(lens), dev(start), 33)
+    torch.cuda.synchronize()
+    ref.bounds(zeros, want, want_s, bt, lens, start, 33)
+    assert np.array_equal(got.cpu().numpy(), want) and np.array_equal(sc.cpu().numpy(), want_s)
+
+
 # ------------------------------------------------------------------ select
 def random_bounds(rng, pages, H, flat=False):
     lo = rng.integers(-127, 100, (pages, H, 1, 128))
