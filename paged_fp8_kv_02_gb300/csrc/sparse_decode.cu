@@ -162,6 +162,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     next_note = 0;
     while (f < f_end) {
       if (slot - slot0 >= 32) {
+        keep_scales();  // the first batch's are still in registers only
         look_up(slot);
         keep_scales();
       }
