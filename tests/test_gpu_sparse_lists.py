@@ -1,5 +1,5 @@
-"""Block-sparse decode where a warp takes more than the 32 entries that it looks
-up at a time: full lists, and lists with gaps in them (padding, pages outside the
+"""Block-sparse and short dense decode where a warp takes more than the 32 pages
+that it looks up at a time: full lists, and lists with gaps in them (padding, pages outside the
 context or the pool)."""
 import numpy as np
 import pytest
@@ -101,3 +101,27 @@ def test_batches_of_few_entries(P, G):
                 sel[b, h, i + rng.choice(32, n, replace=False)] = pages[at:at + n]
                 at += n
     run_lists(rng, pool, lens, G, table, sel, 3, bad if G != 1 else None)
+
+
+@pytest.mark.parametrize("H,G,P,lens", [(8, 1, 16, [16384] * 8), (8, 9, 16, [16384 - 100 * b for b in range(8)]),
+                                        (2, 4, 32, [32768, 30001, 5])])
+def test_short_dense_decode_of_many_pages_a_warp(H, G, P, lens):
+    """Tables that the one-launch kernel takes with contexts as long as they
+    are: about 43 pages a warp for 64 lists of 1024."""
+    import torch
+    p, rng = pf(), np.random.default_rng(P + G)
+    pool, B = Pool(rng, 48, H, P), len(lens)
+    table = rng.integers(0, pool.pages, (B, -(-max(lens) // P))).astype(np.int32)
+    q, qv = bf16(rng.standard_normal((B, H * G, 128)))
+    out, lse = torch.empty_like(q), torch.empty(q.shape[:2], device="cuda")
+    ws = p.paged_decode_attn_scaled(out, q, dev(pool.codes["k"]), dev(pool.codes["v"]), p.SCALE_BLOCK,
+                                    dev(pool.scales["k"]), dev(pool.scales["v"]), dev(table),
+                                    dev(np.array(lens, np.int32)), 0.088, lse_out=lse)
+    torch.cuda.synchronize()
+    assert p.workspace_status(ws) == 0
+    o, l = out.double().cpu().numpy(), lse.double().cpu().numpy()
+    for b, L in enumerate(lens):
+        for h in range(H):
+            heads = slice(h * G, (h + 1) * G)
+            k, v, vs = pool.unit(table[b], h, np.arange(-(-L // P)), L)
+            check_unit(o[b, heads], l[b, heads], qv[b, heads], k, v, vs, 0.088, (b, h))
