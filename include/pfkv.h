@@ -404,11 +404,10 @@ PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *b
  * pages selected[b][h][0 .. top_pages-1].
  *   granularity   PFKV_SCALE_TENSOR, _HEAD or _BLOCK (per token: unsupported)
  *   selected      int32 [batch][num_kv_heads][top_pages], logical pages, each at
- *                 most once, in any order; entries < 0 are padding.  Only the
- *                 first ceil(L_b / page_size) entries count: a list of distinct
- *                 pages has no more.  An entry beyond the context is
- *                 passed over (PFKV_DEVERR_BAD_TOPK), as is a page outside the
- *                 pool (PFKV_DEVERR_BAD_PAGE).
+ *                 most once, in any order; entries < 0 are padding, in any
+ *                 places.  An entry beyond the context is passed over
+ *                 (PFKV_DEVERR_BAD_TOPK), as is a page outside the pool
+ *                 (PFKV_DEVERR_BAD_PAGE).
  *   lse_out       optional fp32 [batch][num_q_heads]
  * No token attended gives out = 0 and lse = -inf.  Numerics as
  * pfkv_paged_decode_attn_scaled per block; results do not depend on what else

@@ -310,7 +310,7 @@ def paged_sparse_decode_attn(out, q, k_cache, v_cache, granularity: int, k_scale
     out/q bf16 [B][Hq][128]; caches uint8 (e4m3) [pages][Hkv][P][128]; scales
     float32 of SCALE_TENSOR [1], SCALE_HEAD [Hkv] or SCALE_BLOCK [pages][Hkv];
     selected int32 [B][Hkv][top_pages], as select_pages writes it (distinct
-    logical pages; entries < 0 are padding).  lse_out: optional float32
+    logical pages in any order; entries < 0 are padding, in any places).  lse_out: optional float32
     [B][Hq]; unit_status: optional int32 [B][Hkv]."""
     import torch
     dev = q.get_device()

@@ -115,9 +115,13 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     L = L < 0 ? 0 : cap;
   }
   const int npages = (L + a.P - 1) / a.P;
-  // listed pages are distinct, so no more than npages entries say anything
+  // The first npages entries, which hold every page of a list without gaps, are
+  // split evenly over the warps; then those behind them, padding but for lists
+  // with gaps (find() below).  All entries split alike would leave most warps of a
+  // short context without work.
   const uint32_t F = (uint32_t)(min(a.K, npages) * tpp);
-  const int f_end = (int)((gw + 1) * F / nw);
+  bool behind = list && a.K > npages;
+  int f_end = (int)((gw + 1) * F / nw);
   int f = (int)(gw * F / nw);  // next tile to issue
   int slot = f / tpp, sub = f - slot * tpp;
 
@@ -158,9 +162,35 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
   // copies; apart, because a stage is free only at the end of an iteration
   const uint64_t kv_policy = l2_evict_first_policy();
   int issued = 0, next_row = 0, next_note = 0;  // next_note 0: there is no tile
+  // the warp's entries behind the first npages, from about the first that is no padding
+  auto go_behind = [&]() {
+    behind = false;
+    const uint32_t rest = (uint32_t)(a.K - npages);
+    const int end = npages + (int)((gw + 1) * rest / nw);
+    int e = npages + (int)(gw * rest / nw);
+    for (; e < end; e += 128) {
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < 4; ++u) {
+        const int i = e + 32 * u + lane;
+        any |= i < end && __ldg(list + i) >= 0;
+      }
+      if (__any_sync(0xFFFFFFFFu, any)) break;
+    }
+    slot = e;
+    slot0 = e - 32;  // to be looked up
+    sub = 0;
+    f = e * tpp;
+    f_end = end * tpp;
+  };
   auto find = [&]() {
     next_note = 0;
-    while (f < f_end) {
+    while (true) {
+      if (f >= f_end) {
+        if (!behind) return;
+        go_behind();
+        continue;
+      }
       if (slot - slot0 >= 32) {
         keep_scales();  // the first batch's are still in registers only
         look_up(slot);

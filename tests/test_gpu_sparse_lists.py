@@ -1,6 +1,6 @@
 """Block-sparse and short dense decode where a warp takes more than the 32 pages
-that it looks up at a time: full lists, and lists with gaps in them (padding, pages outside the
-context or the pool)."""
+that it looks up at a time: full lists, lists with gaps in them (padding, pages
+outside the context or the pool), and lists longer than the context has pages."""
 import numpy as np
 import pytest
 
@@ -125,3 +125,45 @@ def test_short_dense_decode_of_many_pages_a_warp(H, G, P, lens):
             heads = slice(h * G, (h + 1) * G)
             k, v, vs = pool.unit(table[b], h, np.arange(-(-L // P)), L)
             check_unit(o[b, heads], l[b, heads], qv[b, heads], k, v, vs, 0.088, (b, h))
+
+
+def test_pages_after_padding_are_attended():
+    """A list may be longer than the context has pages, with its pages in any
+    places: behind the padding too."""
+    rng = np.random.default_rng(71)
+    pool = Pool(rng, 12, 1, 16)
+    table = rng.integers(0, 12, (4, 9)).astype(np.int32)
+    sel = np.full((4, 1, 8), -1, np.int32)
+    sel[0, 0, :4] = [-1, -1, 0, 1]
+    sel[1, 0] = [-1, 1, -1, -1, -1, -1, -1, 0]
+    sel[2, 0, 7] = 0
+    sel[3, 0] = [2, -3, 0, -1, 9, -1, 1, 400]  # 9 and 400: beyond the context
+    run_lists(rng, pool, [32, 20, 5, 48], 4, table, sel, 3)
+
+
+# clusters of one CTA, of some and of eight; contexts of no page to as many as the list
+@pytest.mark.parametrize("B,H,G,K,P", [(51, 8, 4, 300, 16), (2, 1, 8, 2600, 16), (8, 8, 12, 500, 48), (3, 2, 1, 7, 128)])
+@pytest.mark.parametrize("gran", [0, 3])
+def test_lists_longer_than_the_context(B, H, G, K, P, gran):
+    rng = np.random.default_rng(K + gran)
+    pool = Pool(rng, 40, H, P)
+    npages = rng.integers(0, K + 1, B)
+    npages[:3] = [0, 1, K][:B]
+    lens = [max(0, int(n) * P - int(rng.integers(0, P))) for n in npages]
+    table = rng.integers(0, pool.pages, (B, K + 5)).astype(np.int32)
+    bad = table.copy()
+    outside = rng.random(table.shape) < 0.05
+    bad[outside] = rng.choice([-1, pool.pages], int(outside.sum()))
+    sel = np.full((B, H, K), -1, np.int32)
+    for b in range(B):
+        n = -(-lens[b] // P)
+        for h in range(H):
+            k = int(rng.integers(0, n + 1)) if rng.random() < 0.7 else n
+            # in random places, at the end of the list, or after a run of padding
+            at = (rng.choice(K, k, replace=False), K - 1 - np.arange(k), np.arange(k) + (K - k) // 2)[int(rng.integers(3))]
+            sel[b, h, at] = rng.choice(n, k, replace=False) if n else []
+            if rng.random() < 0.2:
+                free = np.flatnonzero(sel[b, h] < 0)
+                if len(free):
+                    sel[b, h, rng.choice(free)] = K + 1000
+    run_lists(rng, pool, lens, G, table, sel, gran, bad)
