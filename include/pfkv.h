@@ -371,7 +371,8 @@ PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const voi
  * (rint: to nearest, ties to even).  The score is the group's sum of upper
  * bounds of q . k over the page, up to the query's rounding to 8 bits and a
  * factor common to all pages; it is exact in fp32 while the scales are powers
- * of two, so equal scores are ties, and ties go to the lower page.  The first
+ * of two (beyond fp32's range it counts as its largest number of that sign), so
+ * equal scores are ties, and ties go to the lower page.  The first
  * sink_pages and the last recent_pages pages are listed whatever their score.
  *   selected      int32 [batch][num_kv_heads][top_pages], written: logical
  *                 pages t / page_size in ascending order, then -1 where the

@@ -14,7 +14,8 @@
 // positive and one negative query: 256 products a page however many heads.
 // Numbers are integers of 8 bits, sums stay below 2^23 and the scales are powers
 // of two, so a score is exact and the same in any order of summation: ties are
-// real ties, and go to the lower page.
+// real ties, and go to the lower page.  A score beyond fp32's range (keys above
+// about 2^100) counts as the largest number.
 //
 // Two stages.  Scores: a warp takes some tens of consecutive pages of one
 // (request, KV head), makes the 8-bit query for itself, and reads the 256 bytes
@@ -266,6 +267,8 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
       } else if (score != score) {
         score = -INFINITY;  // a page outside the pool, a scale that is none
       } else {
+        // beyond the range: the largest number, so that the infinities keep their meaning
+        score = fminf(fmaxf(score, -FLT_MAX), FLT_MAX);
         low = fminf(low, score);
         high = fmaxf(high, score);
       }
@@ -276,7 +279,8 @@ __device__ __forceinline__ bool score_block(const SelectArgs& a, ScoreShared& sh
   for (int g = 0; 32 * g < count; ++g) {
     const Group nxt = look_up(g + 1, pages_next);
     pages_next = entries(g + 2);
-    const float scale = cur.bs * cur.ks;
+    float scale = cur.bs * cur.ks;
+    if (scale > FLT_MAX) scale = FLT_MAX;  // products with 0 stay 0
     load(y, cur, g, 1);
     sum_up(x, scale, g, 0);
     load(x, cur, g, 2);
