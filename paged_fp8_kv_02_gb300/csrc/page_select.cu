@@ -711,6 +711,10 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   a.num_pages = num_pages;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   const int sms = device_sm_count();
+  if (sms <= 0) {
+    const int rc = check_cuda("select_pages device query");
+    return rc != PFKV_OK ? rc : fail(PFKV_ERR_CUDA, "select_pages: no device");
+  }
   cudaLaunchAttribute attr[1];
   cudaLaunchConfig_t cfg = {};
   cfg.stream = s;

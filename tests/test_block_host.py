@@ -1,0 +1,45 @@
+"""Host side of the block-sparse calls without a GPU: limits, a process without
+a device, and the device that a workspace is sized for (CPU only)."""
+import ctypes
+import os
+import subprocess
+import sys
+import textwrap
+
+import pytest
+
+ROOT = os.path.dirname(os.path.dirname(os.path.abspath(__file__)))
+
+
+def without_device(code):
+    """Run code in a process that sees no GPU, so that no launch can happen."""
+    env = dict(os.environ, CUDA_VISIBLE_DEVICES="")
+    head = f"""
+        import ctypes, sys
+        sys.path.insert(0, {ROOT!r})
+        import paged_fp8_kv_02_gb300 as pf
+        from paged_fp8_kv_02_gb300 import _build
+        _build.build_pfkv()
+        lib = pf.load(build_if_missing=False)
+        fake = ctypes.c_void_p(0x10000)
+        i64 = ctypes.c_int64
+    """
+    return subprocess.run([sys.executable, "-c", textwrap.dedent(head) + textwrap.dedent(code)], env=env, cwd=ROOT,
+                          capture_output=True, text=True, timeout=600)
+
+
+SELECT = """
+    def select(Hkv, pages, maxp=9000):
+        return lib.pfkv_select_pages(fake, fake, fake, fake, None, fake, maxp, fake, 2, Hkv, Hkv, 128, 16, i64(pages), 4, 1,
+                                     1, fake, 1 << 30, None, None)
+"""
+
+
+@pytest.mark.parametrize("maxp", [8, 9000])
+def test_select_without_a_device_is_an_error(maxp):
+    r = without_device(SELECT + f"""
+    rc = select(2, 64, {maxp})
+    print(rc, lib.pfkv_last_error().decode())
+    """)
+    assert r.returncode == 0, (r.returncode, r.stderr)
+    assert r.stdout.startswith("-3 select_pages"), r.stdout
