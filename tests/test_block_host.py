@@ -43,3 +43,17 @@ def test_select_without_a_device_is_an_error(maxp):
     """)
     assert r.returncode == 0, (r.returncode, r.stderr)
     assert r.stdout.startswith("-3 select_pages"), r.stdout
+
+
+def test_the_other_calls_without_a_device_are_errors():
+    r = without_device("""
+    print(lib.pfkv_kv_append_fp8_block(fake, fake, fake, fake, fake, fake, fake, 8, fake, fake, 2, 4, 2, 2, 128, 16,
+                                       i64(64), None))
+    print(lib.pfkv_page_key_bounds(fake, fake, fake, fake, 8, fake, fake, 2, 2, 2, 128, 16, i64(64), None))
+    print(lib.pfkv_paged_sparse_decode_attn(fake, fake, fake, fake, 3, fake, fake, fake, 4, fake, 8, fake, 2, 16, 2, 128,
+                                            16, i64(64), 0.1, None, None, None))
+    for maxp in (8, 9000):
+        print(lib.pfkv_paged_decode_attn_scaled(fake, fake, fake, fake, 3, fake, fake, fake, maxp, fake, 2, 16, 2, 128, 16,
+                                                i64(64), 0.1, 0, fake, 1 << 30, None, None))
+    """)
+    assert r.returncode == 0 and r.stdout.split() == ["-3"] * 5, (r.returncode, r.stdout, r.stderr)
