@@ -673,7 +673,7 @@ extern "C" int pfkv_select_pages(int32_t* selected, const void* q, const int8_t*
   if (head_dim != kD) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: head_dim %d != 128", head_dim);
   if ((int64_t)max_pages_per_seq * page_size >= (int64_t)1 << 30)
     return fail(PFKV_ERR_UNSUPPORTED, "select_pages: block table too long");
-  if (num_pages > ((int64_t)1 << 31) / num_kv_heads - 1)
+  if (num_pages > (((int64_t)1 << 31) - 1) / num_kv_heads)
     return fail(PFKV_ERR_UNSUPPORTED, "select_pages: 2^31 or more (page, KV head) pairs");
   const int64_t units = (int64_t)batch * num_kv_heads;
   if (units > 0x7FFFFFFF) return fail(PFKV_ERR_UNSUPPORTED, "select_pages: batch too large");

@@ -57,3 +57,14 @@ def test_the_other_calls_without_a_device_are_errors():
                                                 i64(64), 0.1, 0, fake, 1 << 30, None, None))
     """)
     assert r.returncode == 0 and r.stdout.split() == ["-3"] * 5, (r.returncode, r.stdout, r.stderr)
+
+
+def test_select_takes_every_pool_below_two_to_the_31_pairs():
+    """Up to 2^31 - 1 (page, KV head) pairs, also where the heads do not divide
+    2^31; -3 is the missing device."""
+    r = without_device(SELECT + """
+    for heads in (1, 2, 3, 5, 7, 8, 48):
+        most = (2 ** 31 - 1) // heads
+        print(select(heads, most), select(heads, most + 1))
+    """)
+    assert r.returncode == 0 and r.stdout.splitlines() == ["-3 -2"] * 7, (r.returncode, r.stdout, r.stderr)
