@@ -197,6 +197,15 @@ def _want(name: str, t, dtype, shape, device: int) -> int:
                      f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _on(device: int, f, *args):
+    """f(*args) with `device` the current one."""
+    import torch
+    if device == torch._C._cuda_getDevice():
+        return f(*args)
+    with torch.cuda.device(device):
+        return f(*args)
+
+
 def _call(fn: str, device: int, stream, *args):
     """One entry point on a device: its current stream unless one is given."""
     import torch
@@ -208,13 +217,7 @@ def _call(fn: str, device: int, stream, *args):
         raise ValueError(f"{fn}: the stream belongs to {stream.device}, the tensors to device {device}")
     else:
         handle = stream.cuda_stream
-    f = getattr(_lib or load(), "pfkv_" + fn)
-    if device == torch._C._cuda_getDevice():
-        rc = f(*args, handle)
-    else:
-        with torch.cuda.device(device):
-            rc = f(*args, handle)
-    _check(fn, rc)
+    _check(fn, _on(device, getattr(_lib or load(), "pfkv_" + fn), *args, handle))
 
 
 def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, block_tables, context_lens, new_start,
@@ -267,6 +270,7 @@ def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, n
 
 
 def select_pages_workspace_size(batch: int, num_kv_heads: int, max_pages_per_seq: int) -> int:
+    """Bytes of scratch that select_pages needs on the current device."""
     return int(load().pfkv_select_pages_workspace_size(batch, num_kv_heads, max_pages_per_seq))
 
 
@@ -286,7 +290,9 @@ def select_pages(selected, q, bounds, bound_scales, block_tables, context_lens, 
     maxp, top = block_tables.shape[1], selected.shape[2]
     nbytes = 0
     if workspace is None:
-        nbytes = (_lib or load()).pfkv_select_pages_workspace_size(B, Hkv, maxp)
+        if dev < 0:
+            raise ValueError("expected CUDA tensors")
+        nbytes = _on(dev, (_lib or load()).pfkv_select_pages_workspace_size, B, Hkv, maxp)
         if nbytes:
             workspace = torch.empty(nbytes, dtype=torch.uint8, device=q.device)
             if stream is not None:  # a caller that drops it gives it back while that stream may still use it

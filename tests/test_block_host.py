@@ -1,6 +1,5 @@
 """Host side of the block-sparse calls without a GPU: limits, a process without
 a device, and the device that a workspace is sized for (CPU only)."""
-import ctypes
 import os
 import subprocess
 import sys
@@ -68,3 +67,66 @@ def test_select_takes_every_pool_below_two_to_the_31_pairs():
         print(select(heads, most), select(heads, most + 1))
     """)
     assert r.returncode == 0 and r.stdout.splitlines() == ["-3 -2"] * 7, (r.returncode, r.stdout, r.stderr)
+
+
+class FakeTensor:
+    """Shape, type and place of a tensor on a device that is not there."""
+
+    def __init__(self, shape, dtype, device):
+        self.shape, self.dtype, self._device = tuple(shape), dtype, device
+        self.device = f"cuda:{device}"
+
+    def get_device(self):
+        return self._device
+
+    def is_contiguous(self):
+        return True
+
+    def data_ptr(self):
+        return 0x10000
+
+    def numel(self):
+        n = 1
+        for s in self.shape:
+            n *= s
+        return n
+
+
+@pytest.mark.parametrize("current", [0, 1])
+def test_select_sizes_its_workspace_on_the_tensors_device(monkeypatch, current):
+    """A device with other SMs than the current one needs another workspace."""
+    import contextlib
+
+    import torch
+
+    import paged_fp8_kv_02_gb300 as pf
+    state = {"device": current}
+    calls = []
+
+    @contextlib.contextmanager
+    def device(d):
+        before, state["device"] = state["device"], d
+        yield
+        state["device"] = before
+
+    class Lib:
+        @staticmethod
+        def pfkv_select_pages_workspace_size(*args):
+            calls.append(("size", state["device"], args))
+            return 512 << state["device"]
+
+        @staticmethod
+        def pfkv_select_pages(*args):
+            calls.append(("call", state["device"], args))
+            return 0
+
+    monkeypatch.setattr(pf, "_lib", Lib)
+    monkeypatch.setattr(torch.cuda, "device", device)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: state["device"], raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 77 + d, raising=False)
+    monkeypatch.setattr(torch, "empty", lambda n, dtype, device: FakeTensor((n,), dtype, int(device[5:])))
+    T = lambda dt, *s: FakeTensor(s, dt, 1)
+    ws = pf.select_pages(T(torch.int32, 2, 4, 8), T(torch.bfloat16, 2, 16, 128), T(torch.int8, 9, 4, 2, 128),
+                         T(torch.float32, 9, 4), T(torch.int32, 2, 9000), T(torch.int32, 2), 16)
+    assert [c[:2] for c in calls] == [("size", 1), ("call", 1)] and state["device"] == current
+    assert ws.numel() == 1024 and calls[0][2] == (2, 4, 9000) and calls[1][2][-1] == 78 and 1024 in calls[1][2]
