@@ -300,7 +300,10 @@ PFKV_API int pfkv_paged_decode_attn_noalloc(void *out, const void *q, const void
  * probability before the f16 P.V product (the accumulator is rescaled when
  * that largest scale grows, as for the running maximum of the softmax).
  * Per block: two loads per 16-token tile, each K scale on the tile's raw
- * scores, V scales as weights as per token; 8 / page_size extra bytes per row.
+ * scores, and the V scale inside the exponent of the probability that enters
+ * the f16 P.V product, whose unit follows the head's largest probability times
+ * V scale: a term is rounded by 2^-11 of itself or 2^-25 of that largest;
+ * 8 / page_size extra bytes per row.
  * Numerics: per tensor and per head as pfkv_paged_decode_attn; per token and
  * per block, the
  * score products are f16 on K widened in registers, against q times one

@@ -41,6 +41,7 @@
 
 #include "pfkv_internal.h"
 #include "pfkv_ptx.cuh"
+#include "pfkv_tile.cuh"
 
 namespace pfkv {
 namespace {
@@ -61,7 +62,7 @@ constexpr float kLog2e = 1.4426950408889634f;
 // (page, KV head).
 enum : int { kSclHost = 0, kSclUnit = 1, kSclToken = 2, kSclBlock = 3 };
 constexpr int kScaleStageBytes = 128;  // per-token mode: 16 K + 16 V fp32 scales per stage
-constexpr int kBlockScaleBytes = 8;    // per-block mode: the tile's K and V scale
+constexpr int kBlockScaleBytes = 8;    // per-block mode: the tile's K scale, log2 of its V scale
 constexpr float kLn2 = 0.6931471805599453f;
 
 struct DecodeArgs {
@@ -251,7 +252,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
   const uint32_t wbase = smem_base + warp * Geo::kWarpBytes;
   uint8_t* const wptr = smem_raw + (smem_base - smem_u32(smem_raw)) + warp * Geo::kWarpBytes;
   // per-token mode: this warp's kStages x (16 K + 16 V) fp32 scales; per-block
-  // mode: kStages x (K, V)
+  // mode: kStages x (K, log2 V)
   const uint32_t sbase = smem_base + kWarps * Geo::kWarpBytes + warp * Geo::kScaleWarpBytes;
   float* const sptr = reinterpret_cast<float*>(wptr + (kWarps - warp) * Geo::kWarpBytes +
                                                warp * Geo::kScaleWarpBytes);
@@ -295,7 +296,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
   auto store_pending = [&]() {
     if constexpr (kScl == kSclBlock) {
       if (lane == 0 && pend_stage >= 0) {
-        *reinterpret_cast<float2*>(sptr + 2 * pend_stage) = make_float2(pend_k, pend_v);
+        *reinterpret_cast<float2*>(sptr + 2 * pend_stage) = make_float2(pend_k, __log2f(pend_v));
         pend_stage = -1;
       }
     }
@@ -373,7 +374,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
 #pragma unroll
   for (int j = 0; j < NT; ++j) qinv[j][0] = qinv[j][1] = 1.f;
   float unit_vs = 1.f;       // unit mode: the unit's V scale
-  float vref = 0.f, vinv = 0.f;  // token and block modes: largest V scale of the unit so far, 1 / it
+  float vref = 0.f, vinv = 0.f;  // token mode: largest V scale of the unit so far, 1 / it
+  float cref[NT][2];             // block mode: reference of scores plus log2 of the V scale
 
   auto flush = [&](int64_t f_stop) {
     // f_stop: first flattened tile after this segment; cc is on its last tile
@@ -388,7 +390,8 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
     const int nchunks = (int)((a.unit_start[b + 1] - a.unit_start[b]) / a.Hkv);
     const bool final = (nchunks == 1) && seg_begin == s_u && f_stop == e_u;
     // factor from accumulator units to dequantised V units
-    const float vmul = kScl == kSclUnit ? unit_vs : (kScl == kSclToken || kScl == kSclBlock ? vref : 1.f);
+    // (block mode: per head, below)
+    const float vmul = kScl == kSclUnit ? unit_vs : (kScl == kSclToken ? vref : 1.f);
 #pragma unroll
     for (int j = 0; j < NT; ++j)
 #pragma unroll
@@ -420,8 +423,9 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
           vals[2 * i + 1] = o[j][i][2 + e];
         }
         if constexpr (kScl != kSclHost) {
+          const float to_v = kScl == kSclBlock ? tile::unit(mref[j][e], cref[j][e]) : vmul;
 #pragma unroll
-          for (int i = 0; i < 16; ++i) vals[i] *= vmul;
+          for (int i = 0; i < 16; ++i) vals[i] *= to_v;
         }
         if (final) {
           const float inv = a.out_scale / l[j][e];
@@ -467,7 +471,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
       sc = __ldg(a.k_scales + si) * a.logit_scale;
       unit_vs = __ldg(a.v_scales + si);
     }
-    if constexpr (kScl == kSclToken || kScl == kSclBlock) {
+    if constexpr (kScl == kSclToken) {
       vref = 0.f;
       vinv = 0.f;
     }
@@ -475,6 +479,7 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
     for (int j = 0; j < NT; ++j) {
       mref[j][0] = mref[j][1] = -INFINITY;
       rthr[j][0] = rthr[j][1] = -INFINITY;
+      if constexpr (kScl == kSclBlock) cref[j][0] = cref[j][1] = tile::kNoUnit;
       l[j][0] = l[j][1] = 0.f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
@@ -697,50 +702,51 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
         if (!vb8) vs8 = 0.f;
       }
     }
-    bool grow = false;
+    if constexpr (kScl == kSclBlock) {
+      tile::raise_references<NT>(s, sc, sptr[2 * stage + 1], kRescaleLog2, mref, cref, l, o);
+    } else {
+      bool grow = false;
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-      grow |= (fmaxf(s[j][0], s[j][2]) > rthr[j][0]) | (fmaxf(s[j][1], s[j][3]) > rthr[j][1]);
-    if (__any_sync(0xFFFFFFFFu, grow)) {
+      for (int j = 0; j < NT; ++j)
+        grow |= (fmaxf(s[j][0], s[j][2]) > rthr[j][0]) | (fmaxf(s[j][1], s[j][3]) > rthr[j][1]);
+      if (__any_sync(0xFFFFFFFFu, grow)) {
 #pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float mx0 = fmaxf(s[j][0], s[j][2]), mx1 = fmaxf(s[j][1], s[j][3]);
+        for (int j = 0; j < NT; ++j) {
+          float mx0 = fmaxf(s[j][0], s[j][2]), mx1 = fmaxf(s[j][1], s[j][3]);
 #pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
+          for (int off = 4; off < 32; off <<= 1) {
+            mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
+            mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
+          }
+          const float mn0 = fmaxf(mref[j][0], mx0 * sc), mn1 = fmaxf(mref[j][1], mx1 * sc);
+          const float al0 = fast_exp2(mref[j][0] - mn0), al1 = fast_exp2(mref[j][1] - mn1);
+          l[j][0] *= al0;
+          l[j][1] *= al1;
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            o[j][i][0] *= al0;
+            o[j][i][1] *= al1;
+            o[j][i][2] *= al0;
+            o[j][i][3] *= al1;
+          }
+          mref[j][0] = mn0;
+          mref[j][1] = mn1;
+          rthr[j][0] = (mn0 + kRescaleLog2) / sc;
+          rthr[j][1] = (mn1 + kRescaleLog2) / sc;
         }
-        const float mn0 = fmaxf(mref[j][0], mx0 * sc), mn1 = fmaxf(mref[j][1], mx1 * sc);
-        const float al0 = fast_exp2(mref[j][0] - mn0), al1 = fast_exp2(mref[j][1] - mn1);
-        l[j][0] *= al0;
-        l[j][1] *= al1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[j][i][0] *= al0;
-          o[j][i][1] *= al1;
-          o[j][i][2] *= al0;
-          o[j][i][3] *= al1;
-        }
-        mref[j][0] = mn0;
-        mref[j][1] = mn1;
-        rthr[j][0] = (mn0 + kRescaleLog2) / sc;
-        rthr[j][1] = (mn1 + kRescaleLog2) / sc;
       }
     }
-    // per-token and per-block V scales enter as weights on p relative to vref, the largest V
+    // per-token V scales enter as weights on p relative to vref, the largest V
     // scale of the unit so far, so that p * weight <= p stays in f16 range;
     // when vref grows the accumulator is rescaled like the running maximum
     float w0 = 1.f, w8 = 1.f;
-    if constexpr (kScl == kSclToken || kScl == kSclBlock) {
-      // the largest V scale of the tile; per block it is the tile's only one.
-      // Per token, with one or two heads per KV head the
+    if constexpr (kScl == kSclToken) {
+      // the largest V scale of the tile: with one or two heads per KV head the
       // tile's work is too short to hide a shuffle chain, so every thread
       // reads the tile's 16 V scales from the stage; with more heads the
       // chain is hidden and costs fewer instructions
       float vm;
-      if constexpr (kScl == kSclBlock) {
-        vm = vs0 = vs8 = sptr[2 * stage + 1];
-      } else if (a.G <= 2) {
+      if (a.G <= 2) {
         const float4* vp = reinterpret_cast<const float4*>(sptr + stage * (kScaleStageBytes / 4) + 16);
         float4 q4[4] = {vp[0], vp[1], vp[2], vp[3]};
         if (partial) {
@@ -788,11 +794,18 @@ __global__ void __launch_bounds__(kWarps * 32, NT == 1 ? 4 : 2)
       float p3 = fast_exp2(fmaf(s[j][3], sc, -mref[j][1]));
       l[j][0] += p0 + p2;
       l[j][1] += p1 + p3;
-      if constexpr (kScl == kSclToken || kScl == kSclBlock) {
+      if constexpr (kScl == kSclToken) {
         p0 *= w0;
         p1 *= w0;
         p2 *= w8;
         p3 *= w8;
+      }
+      if constexpr (kScl == kSclBlock) {  // the V scale beside the score
+        const float d0 = sptr[2 * stage + 1] - cref[j][0], d1 = sptr[2 * stage + 1] - cref[j][1];
+        p0 = fast_exp2(fmaf(s[j][0], sc, d0));
+        p1 = fast_exp2(fmaf(s[j][1], sc, d1));
+        p2 = fast_exp2(fmaf(s[j][2], sc, d0));
+        p3 = fast_exp2(fmaf(s[j][3], sc, d1));
       }
       if constexpr (kBf16) {
         pb[j][0] = movmatrix_trans(pack_bf16x2(p0, p1));

@@ -7,6 +7,7 @@
 // O^T[128 x 8] per head tile: o[j][i][e] and o[j][i][2 + e] are head_dim values
 // 16g + 2i and 16g + 2i + 1 of head 8j + 2t + e.
 #pragma once
+#include <math.h>
 #include <stdint.h>
 
 #include "pfkv_ptx.cuh"
@@ -96,6 +97,57 @@ __device__ __forceinline__ void scores(const uint8_t* kb, int lane, const uint32
 #pragma unroll
     for (int i = 0; i < 4; ++i) s[j][i] += r[j][i];
 }
+
+// Softmax where every page has a V scale of its own.  A head column keeps two
+// references in log2 units: m of the scores, and c of scores plus log2 of the V
+// scale.  l is a sum of 2^(s - m), o one of 2^(s + log2 vs - c) times V's codes, so
+//   out = (o 2^(c - m)) / l.
+// The terms of o are rounded to f16, so their unit has to follow the largest p vs:
+// relative to the largest V scale alone, a page of small values would lose its bits,
+// or vanish, beside one of large values, however small the probability of that one.
+// One exponential takes s + log2 vs - c: of the product 2^(s - m) times vs 2^(m - c)
+// one factor can underflow where the other overflows.  c >= m - 126 keeps 2^(c - m)
+// a normal number.
+constexpr float kNoUnit = -3.0e38f;  // c before the first token
+
+// Both references of the columns that a tile's scores s (raw; times sc they are in
+// log2 units) exceed by more than `slack` are raised, and l and o follow.  lvs:
+// log2 of the tile's V scale, -inf where that is 0.
+template <int NT>
+__device__ __forceinline__ void raise_references(const float (&s)[NT][4], float sc, float lvs, float slack,
+                                                 float (&m)[NT][2], float (&c)[NT][2], float (&l)[NT][2],
+                                                 float (&o)[NT][8][4]) {
+  bool grow = false;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      const float x = fmaxf(s[j][e], s[j][2 + e]);
+      grow |= (fmaf(x, sc, -m[j][e]) > slack) | (fmaf(x, sc, lvs - c[j][e]) > slack);
+    }
+  if (!__any_sync(0xFFFFFFFFu, grow)) return;
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float x = fmaxf(s[j][e], s[j][2 + e]);
+#pragma unroll
+      for (int off = 4; off < 32; off <<= 1) x = fmaxf(x, __shfl_xor_sync(0xFFFFFFFFu, x, off));
+      x *= sc;
+      const float mn = fmaxf(m[j][e], x), cn = fmaxf(fmaxf(c[j][e], x + lvs), mn - 126.f);
+      l[j][e] *= fast_exp2(m[j][e] - mn);
+      const float r = fast_exp2(c[j][e] - cn);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        o[j][i][e] *= r;
+        o[j][i][2 + e] *= r;
+      }
+      m[j][e] = mn;
+      c[j][e] = cn;
+    }
+}
+// Factor from o's unit to p times V; 0 where no token was met.
+__device__ __forceinline__ float unit(float m, float c) { return m == -INFINITY ? 0.f : fast_exp2(c - m); }
 
 // o += V^T P^T over the tile's first n tokens (rows past them may hold any
 // bytes, NaN codes too, and are taken as zeros).  pb: P^T fragments in f16.

@@ -47,8 +47,9 @@ constexpr int kStateFloats = kD + 4;  // of a head: o, m, l; whole 16-byte piece
 static_assert(kMaxG * kStateFloats * 4 <= kWarpBytes, "a warp's state fits its ring");
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
-// A head's reference maximum is only raised when a score exceeds it by more
-// than this (log2 units), so p stays at most 2^8: exact enough in f16 and f32.
+// A head's references (pfkv_tile.cuh) are only raised when a token exceeds one by
+// more than this (log2 units), so p and p vs stay at most 2^8 units: exact enough in
+// f16 and f32.
 constexpr float kRescaleLog2 = 8.f;
 
 struct SparseArgs {
@@ -75,7 +76,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
   extern __shared__ uint8_t smem_raw[];
   __shared__ __align__(8) uint64_t bars[kWarps][kStages];
   __shared__ int meta[kWarps][kStages];          // of the stage's tile: tokens << 8 | its page's place in scales
-  __shared__ float2 scales[kWarps][kBatches * 32];  // K and V scales of the last batches of pages looked up
+  __shared__ float2 scales[kWarps][kBatches * 32];  // K scale, log2 of the V scale: the last batches of pages looked up
   __shared__ uint32_t err;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
@@ -155,7 +156,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
     // a batch with tokens gets the next place; the last kStages of those stay
     if (__any_sync(0xFFFFFFFFu, tokens > 0)) place = (place + 32) % (kBatches * 32);
   };
-  auto keep_scales = [&]() { scales[warp][place + lane] = make_float2(ks, vs); };
+  auto keep_scales = [&]() { scales[warp][place + lane] = make_float2(ks, __log2f(vs)); };
   if (f < f_end) look_up(slot);
 
   // ---------------- producer: find() the next tile with tokens, then issue() its
@@ -236,19 +237,17 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
 
   // ---------------- consumer
   uint32_t qf[NT][8][2];
-  float qinv[NT][2], mref[NT][2], rthr[NT][2], l[NT][2], o[NT][8][4];
+  float qinv[NT][2], mref[NT][2], cref[NT][2], l[NT][2], o[NT][8][4];
   tile::scale_q<NT>(qrow, lane, qf, qinv);
 #pragma unroll
   for (int j = 0; j < NT; ++j) {
-    mref[j][0] = mref[j][1] = rthr[j][0] = rthr[j][1] = -INFINITY;
+    mref[j][0] = mref[j][1] = -INFINITY;
+    cref[j][0] = cref[j][1] = tile::kNoUnit;
     l[j][0] = l[j][1] = 0.f;
 #pragma unroll
     for (int i = 0; i < 8; ++i) o[j][i][0] = o[j][i][1] = o[j][i][2] = o[j][i][3] = 0.f;
   }
-  // V scales enter as weights on p relative to vref, the largest so far, so that
-  // p keeps f16's range; o is rescaled when vref grows
-  float vref = 0.f, vinv = 0.f;
-  const float sc = a.logit_scale, inv_sc = 1.f / sc;
+  const float sc = a.logit_scale;
   int stage = 0, done = 0;
   uint32_t phase = 0;
   bool timed_out = false;
@@ -275,51 +274,7 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
         if (g + 8 >= n) s[j][2] = s[j][3] = -INFINITY;
       }
     }
-    bool grow = false;
-#pragma unroll
-    for (int j = 0; j < NT; ++j)
-      grow |= (fmaxf(s[j][0], s[j][2]) > rthr[j][0]) | (fmaxf(s[j][1], s[j][3]) > rthr[j][1]);
-    if (__any_sync(0xFFFFFFFFu, grow)) {
-#pragma unroll
-      for (int j = 0; j < NT; ++j) {
-        float mx0 = fmaxf(s[j][0], s[j][2]), mx1 = fmaxf(s[j][1], s[j][3]);
-#pragma unroll
-        for (int off = 4; off < 32; off <<= 1) {
-          mx0 = fmaxf(mx0, __shfl_xor_sync(0xFFFFFFFFu, mx0, off));
-          mx1 = fmaxf(mx1, __shfl_xor_sync(0xFFFFFFFFu, mx1, off));
-        }
-        const float m0 = fmaxf(mref[j][0], mx0 * sc), m1 = fmaxf(mref[j][1], mx1 * sc);
-        const float a0 = fast_exp2(mref[j][0] - m0), a1 = fast_exp2(mref[j][1] - m1);
-        l[j][0] *= a0;
-        l[j][1] *= a1;
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[j][i][0] *= a0;
-          o[j][i][1] *= a1;
-          o[j][i][2] *= a0;
-          o[j][i][3] *= a1;
-        }
-        mref[j][0] = m0;
-        mref[j][1] = m1;
-        rthr[j][0] = (m0 + kRescaleLog2) * inv_sc;
-        rthr[j][1] = (m1 + kRescaleLog2) * inv_sc;
-      }
-    }
-    if (scale.y > vref) {  // warp-uniform
-      vinv = 1.f / scale.y;
-      const float r = vref * vinv;
-#pragma unroll
-      for (int j = 0; j < NT; ++j)
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-          o[j][i][0] *= r;
-          o[j][i][1] *= r;
-          o[j][i][2] *= r;
-          o[j][i][3] *= r;
-        }
-      vref = scale.y;
-    }
-    const float w = scale.y * vinv;
+    tile::raise_references<NT>(s, sc, scale.y, kRescaleLog2, mref, cref, l, o);
     uint32_t pb[NT][2];
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
@@ -327,8 +282,9 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
       const float p2 = fast_exp2(fmaf(s[j][2], sc, -mref[j][0])), p3 = fast_exp2(fmaf(s[j][3], sc, -mref[j][1]));
       l[j][0] += p0 + p2;
       l[j][1] += p1 + p3;
-      pb[j][0] = movmatrix_trans(pack_f16x2(p0 * w, p1 * w));
-      pb[j][1] = movmatrix_trans(pack_f16x2(p2 * w, p3 * w));
+      const float d0 = scale.y - cref[j][0], d1 = scale.y - cref[j][1];
+      pb[j][0] = movmatrix_trans(pack_f16x2(fast_exp2(fmaf(s[j][0], sc, d0)), fast_exp2(fmaf(s[j][1], sc, d1))));
+      pb[j][1] = movmatrix_trans(pack_f16x2(fast_exp2(fmaf(s[j][2], sc, d0)), fast_exp2(fmaf(s[j][3], sc, d1))));
     }
     tile::accumulate<NT>(kb + tile::kSlabBytes, lane, n, pb, o);
     // every load of the stage has returned (its values are in use): it can be
@@ -368,10 +324,11 @@ __global__ void __launch_bounds__(kWarps * 32, (NT == 1 ? 16 : 8) / kWarps)
       const int head = 8 * j + 2 * t + e;
       if (head < a.G) {
         float4* d = reinterpret_cast<float4*>(st + head * kD + 16 * g);
+        const float unit = tile::unit(mref[j][e], cref[j][e]);
 #pragma unroll
         for (int k = 0; k < 4; ++k)
-          d[k] = make_float4(o[j][2 * k][e] * vref, o[j][2 * k][2 + e] * vref, o[j][2 * k + 1][e] * vref,
-                             o[j][2 * k + 1][2 + e] * vref);
+          d[k] = make_float4(o[j][2 * k][e] * unit, o[j][2 * k][2 + e] * unit, o[j][2 * k + 1][e] * unit,
+                             o[j][2 * k + 1][2 + e] * unit);
         if (g == 0) {
           st[a.G * kD + 2 * head] = mref[j][e];
           st[a.G * kD + 2 * head + 1] = v;

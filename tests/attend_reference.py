@@ -1,6 +1,6 @@
 """Attention over pages of an e4m3 cache in 64 bits, with the bound that the
 warp-level kernels' arithmetic allows: K widened to f16 against Q in f16, the
-probabilities times their V weight in f16, everything summed in fp32."""
+probabilities times their V scale in f16, everything summed in fp32."""
 from __future__ import annotations
 
 import numpy as np
@@ -56,12 +56,13 @@ def attend(q, keys, values, vs, softmax_scale):
     # bits), and the scales, log2(e) and the exponent's fma another 4 x 2^-24.
     mag = np.abs(q) @ np.abs(keys).T
     ds = softmax_scale * (mag * (130 * 2.0 ** -23) + np.abs(q).max() * 2.0 ** -39 * np.abs(keys).sum(1)).max(1)[:, None]
-    # Terms.  p w rounded to f16: 2^-11 of itself, or half a subnormal step,
-    # 2^-25, relative to a weight unit that is no more than the largest p vs of
-    # the rows.  A score error ds changes a weight and their sum by e^ds - 1
-    # each; T additions of the output lose 2^-23 each (truncated), those of the
-    # denominator 2^-24; exponentials, rescaling and the join 2^-18.
-    rel = 2.0 ** -11 + 2 * np.expm1(ds) + 1.5 * T * 2.0 ** -23 + 2.0 ** -18
+    # Terms.  p vs rounded to f16: 2^-11 of itself, or half a subnormal step,
+    # 2^-25, of a unit that is no more than the largest p vs of the rows.  A score
+    # error ds changes a term and the sum of p by e^ds - 1 each; T additions of
+    # the output lose 2^-23 each (truncated), those of the denominator 2^-24; the
+    # logarithm of a V scale (up to 126 in magnitude) and its sums, exponentials
+    # and the join 2^-16.
+    rel = 2.0 ** -11 + 2 * np.expm1(ds) + 1.5 * T * 2.0 ** -23 + 2.0 ** -16
     unit = (p * vs).max(1, keepdims=True) / den
     codes = (np.abs(values) / np.where(vs > 0, vs, 1.0)[:, None]).sum(0)
     bound = p @ np.abs(values) / den * rel + unit * codes * 2.0 ** -25 + np.abs(out) * 2.0 ** -8 + 2.0 ** -133
