@@ -63,31 +63,41 @@ def run(rng, pool, lens, G, width, split, favoured, lead, spread_of_heads=False)
                 check_unit(o[b, heads], l[b, heads], qv[b, heads], k, v, vs, 0.088, (call, b, h))
 
 
-# tables for the one-launch kernel, for the kernel with a plan and a merge, and in chunks
-@pytest.mark.parametrize("width,split", [(64, 0), (4096, 0), (4096, 64)])
-@pytest.mark.parametrize("G", [1, 4, 12])
-@pytest.mark.parametrize("binades", [15, 26, 60, 110])
+# 408 lists, so that a warp meets many pages of one list; tables for the one-launch
+# kernel, for the kernel with a plan and a merge, and in chunks
+B, H = 51, 8
+FORMS = pytest.mark.parametrize("width,split", [(64, 0), (4096, 0), (4096, 128)])
+
+
+def lengths(rng):
+    return [16 * 40, 16] + [int(n) for n in rng.integers(16 * 20, 16 * 48, B - 2)]
+
+
+@FORMS
+@pytest.mark.parametrize("G", [1, 12])
+@pytest.mark.parametrize("binades", [15, 26, 110])
 def test_a_page_of_small_values_with_most_of_the_probability(width, split, G, binades):
     rng = np.random.default_rng(binades + G)
-    lens = [16 * 60, 16 * 41 - 5, 16]
-    pool = Pool(rng, 130, 2, 16, kbin=(-9, -8), vbin=(-4, -2))
-    favoured = [int(rng.integers(0, -(-m // 16))) for m in lens]
-    first = 0
-    for b, m in enumerate(lens):
-        pool.scales["v"][first + favoured[b]] *= 2.0 ** -binades
-        first += -(-m // 16)
+    lens = lengths(rng)
+    pool = Pool(rng, sum(-(-m // 16) for m in lens), H, 16, kbin=(-9, -8), vbin=(-4, -2))
+    favoured, first = [], 0
+    for m in lens:
+        n = -(-m // 16)
+        favoured.append(int(rng.integers(0, n)))
+        pool.scales["v"][first + favoured[-1]] *= 2.0 ** -binades
+        first += n
     run(rng, pool, lens, G, width, split, favoured, lead=binades + 12.0)
 
 
-@pytest.mark.parametrize("width,split", [(64, 0), (4096, 0), (4096, 64)])
+@FORMS
 @pytest.mark.parametrize("spread", [8, 30, 100])
 def test_value_scales_over_many_binades(width, split, spread):
     """Every page its own power; heads that look at one page beside heads that
     look at all of them."""
     rng = np.random.default_rng(spread)
-    lens = [16 * 55, 16 * 50 - 3, 33]
-    pool = Pool(rng, 130, 2, 16, kbin=(-9, -7), vbin=(-spread, 4))
-    run(rng, pool, lens, 8, width, split, [11, 3, 1], lead=30.0, spread_of_heads=True)
+    lens = lengths(rng)
+    pool = Pool(rng, sum(-(-m // 16) for m in lens), H, 16, kbin=(-9, -7), vbin=(-spread, 4))
+    run(rng, pool, lens, 4, width, split, [int(rng.integers(0, -(-m // 16))) for m in lens], lead=30.0, spread_of_heads=True)
 
 
 @pytest.mark.parametrize("width", [64, 4096])
