@@ -186,8 +186,8 @@ PFKV_API int pfkv_kv_append_fp8_scaled(const void *k_new, const void *v_new, voi
  * v_new = v_cache = v_scales = NULL appends K only.  A request with n_b < 0,
  * n_b > max_new_len, n_b > L_b, rows outside [0, num_tokens) or L_b beyond its
  * table is left out, as is a page outside the pool; nothing else is written.
- * A page may receive rows from one request per call (shared prefix pages are
- * full: appends go to a request's own last pages).
+ * A page may receive rows from one request per call, and once (shared prefix
+ * pages are full: appends go to a request's own last pages).
  * Supported: head_dim a multiple of 16, any page_size. */
 PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                                       float *k_scales, float *v_scales, const int32_t *block_tables,
@@ -356,6 +356,8 @@ PFKV_API int pfkv_paged_decode_attn_scaled(void *out, const void *q, const void 
  *   bound_scales  fp32 [num_pages][num_kv_heads], written
  *   k_cache       e4m3 [num_pages][num_kv_heads][page_size][head_dim]
  *   new_start     int32 [batch + 1] (device); max_new_len: host bound on n_b
+ * A page that a call meets more than once (shared by requests) has to hold the
+ * same number of rows each time, as full pages do: its summary is written by each.
  * Requests and pages whose numbers do not fit are left out, as in
  * pfkv_kv_append_fp8_block.  Supported: head_dim 128, any page_size. */
 PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
@@ -389,9 +391,10 @@ PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const voi
  *   workspace     device scratch of at least pfkv_select_pages_workspace_size()
  *                 bytes (query it on the device that will run the call),
  *                 256-byte aligned; contents on entry are ignored.  It holds the
- *                 scores, 4 bytes per KV head and block-table entry; 0 bytes and
- *                 NULL where few short lists keep them on the SMs.  Calls that
- *                 may overlap on the GPU need one each.
+ *                 scores and their ranges, about 6 bytes per KV head and
+ *                 block-table entry; 0 bytes and NULL where few short lists keep
+ *                 them on the SMs.  Calls that may overlap on the GPU need one
+ *                 each.
  * Supported: head_dim 128; G in 1..16; sink_pages + recent_pages <= top_pages;
  * num_pages * num_kv_heads < 2^31; any page_size. */
 PFKV_API size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq);

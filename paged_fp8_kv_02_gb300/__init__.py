@@ -256,7 +256,8 @@ def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, n
     request's last new_start[b+1] - new_start[b] tokens: bounds int8
     [pages][H][2][128] (lower, upper) in units of bound_scales float32
     [pages][H] times the page's K scale, from the e4m3 k_cache uint8
-    [pages][H][P][128].  max_new_len bounds the counts."""
+    [pages][H][P][128].  max_new_len bounds the counts.  A page shared by
+    requests has to hold the same number of rows for each, as full pages do."""
     import torch
     dev = k_cache.get_device()
     pages, H, P, D = k_cache.shape

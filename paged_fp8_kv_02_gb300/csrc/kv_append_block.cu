@@ -75,7 +75,8 @@ __device__ __forceinline__ uint32_t rescale4(uint32_t codes, float f) {
 // One CTA per (request, touched page, head) of K or V.  A thread keeps up to
 // kHold 16-element pieces of the page's new rows in registers between the
 // maximum and the conversion (the launch gives the block enough threads that
-// all of them fit for the page sizes up to 64; larger pages read the rest again).
+// all of them fit for pages of up to 2048 pieces, 256 rows of head_dim 128 or 64 of
+// 512; larger pages read the rest again).
 // The rows' place does not depend on the page, so they are on their way while the
 // block table and the old scale are read.  kChunks: 16-element pieces of a row, or
 // 0 where it is not known beforehand.

@@ -1,6 +1,7 @@
 // page_bounds.cu -- channelwise bounds of the keys of each (page, KV head), in
 // 8-bit integers: the summary from which select_pages scores a page without
-// reading its keys.
+// reading its keys (the summary of Tang et al., "Quest: query-aware sparsity for
+// efficient long-context LLM inference", 2024, here in integers).
 //
 // Over the rows t < L of a page, in units of the page's K scale,
 //   lo_d = min_t K_t[d],  hi_d = max_t K_t[d],  A = max_d max(|lo_d|, |hi_d|),

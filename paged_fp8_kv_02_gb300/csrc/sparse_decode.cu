@@ -7,9 +7,9 @@
 //   out = sum_{t in T} e^{s_t - m} val(V_t) vs(t) / sum_{t in T} e^{s_t - m},
 // with the scales of the tensor, the KV head, or the page.
 //
-// One cluster of up to 8 CTAs per (request, KV head), four warps a CTA.  Each
-// warp takes a contiguous run of the list's 16-token tiles: its lanes look up 32
-// pages at a time (list, block table, scales: one chain of loads for all of
+// One cluster of up to 8 CTAs per (request, KV head), four warps a CTA (eight where
+// there are few lists).  Each warp takes a contiguous run of the list's 16-token
+// tiles: its lanes look up 32 pages at a time (list, block table, scales: one chain of loads for all of
 // them), and a ring of TMA stages of its own keeps its K and V tiles in flight.
 // The warps' states (m, l, o) stay in shared memory and are joined by log-sum-exp
 // through distributed shared memory, so the whole step is one launch without
@@ -18,8 +18,8 @@
 // depend on the length is loaded before it is known, and the first copies are
 // under way before the scales are.
 // Device time: 8 lists of 64 pages x 64 tokens (8.4 MB) 8.2 us; 512 lists of up to 128
-// pages x 16 tokens (203 MB) 37.4 us, 5.4 TB/s; 64 lists of 256 pages x 64 tokens (268 MB)
-// 46.1 us, 5.8 TB/s, each with about 5 us of launch and ramp.  Finding the next tile
+// pages x 16 tokens (203 MB) 37.1 us, 5.5 TB/s; 64 lists of 256 pages x 64 tokens (268 MB)
+// 46.4 us, 5.8 TB/s, each with about 5 us of launch and ramp.  Finding the next tile
 // before the scores instead of after P.V, the states joined per CTA before they
 // cross the cluster, and f16 score products took these from 13.0, 41.4 and 52.2 us.
 #include <cuda_bf16.h>
