@@ -188,7 +188,8 @@ PFKV_API int pfkv_kv_append_fp8_scaled(const void *k_new, const void *v_new, voi
  * table is left out, as is a page outside the pool; nothing else is written.
  * A page may receive rows from one request per call, and once (shared prefix
  * pages are full: appends go to a request's own last pages).
- * Supported: head_dim a multiple of 16, any page_size. */
+ * Supported: head_dim a multiple of 16; any page_size with page_size * head_dim
+ * and max_pages_per_seq * page_size < 2^30. */
 PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void *k_cache, void *v_cache,
                                       float *k_scales, float *v_scales, const int32_t *block_tables,
                                       int max_pages_per_seq, const int32_t *context_lens,
@@ -359,7 +360,8 @@ PFKV_API int pfkv_paged_decode_attn_scaled(void *out, const void *q, const void 
  * A page that a call meets more than once (shared by requests) has to hold the
  * same number of rows each time, as full pages do: its summary is written by each.
  * Requests and pages whose numbers do not fit are left out, as in
- * pfkv_kv_append_fp8_block.  Supported: head_dim 128, any page_size. */
+ * pfkv_kv_append_fp8_block.  bounds starts on 16 bytes.  Supported: head_dim
+ * 128; any page_size with max_pages_per_seq * page_size < 2^30. */
 PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const void *k_cache,
                                   const int32_t *block_tables, int max_pages_per_seq,
                                   const int32_t *context_lens, const int32_t *new_start, int batch,
@@ -396,7 +398,8 @@ PFKV_API int pfkv_page_key_bounds(int8_t *bounds, float *bound_scales, const voi
  *                 them on the SMs.  Calls that may overlap on the GPU need one
  *                 each.
  * Supported: head_dim 128; G in 1..16; sink_pages + recent_pages <= top_pages;
- * num_pages * num_kv_heads < 2^31; any page_size. */
+ * num_pages * num_kv_heads < 2^31; any page_size with max_pages_per_seq *
+ * page_size < 2^30.  bounds starts on 16 bytes. */
 PFKV_API size_t pfkv_select_pages_workspace_size(int batch, int num_kv_heads, int max_pages_per_seq);
 PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *bounds,
                                const float *bound_scales, const float *k_scales,
@@ -419,8 +422,8 @@ PFKV_API int pfkv_select_pages(int32_t *selected, const void *q, const int8_t *b
  * No token attended gives out = 0 and lse = -inf.  Numerics as
  * pfkv_paged_decode_attn_scaled per block; results do not depend on what else
  * runs, but the order of the sums follows the SM count and the sizes.
- * Supported: as pfkv_paged_decode_attn, e4m3 cache; scale arrays 4-byte
- * aligned. */
+ * Supported: as pfkv_paged_decode_attn, e4m3 cache, with max_pages_per_seq and
+ * top_pages times page_size < 2^30; scale arrays 4-byte aligned. */
 PFKV_API int pfkv_paged_sparse_decode_attn(void *out, const void *q, const void *k_cache,
                                            const void *v_cache, pfkv_scale_granularity granularity,
                                            const float *k_scales, const float *v_scales,

@@ -41,7 +41,7 @@
 // kernels with the scores in the workspace: the first is spread evenly over all SMs
 // with neighbouring warps on neighbouring heads, so that a page's bounds are read
 // as one run, and the second is resident and waiting when the first ends.
-// Device time: one request of 128K tokens (8 lists of 2K pages) 7.6 us, a chain of
+// Device time: one request of 128K tokens (8 lists of 2K pages) 7.9 us, a chain of
 // loads and block barriers; 64 requests of up to 32K tokens (512 lists of up to 2K
 // pages, 55 MB) 20.4 us, of which the list takes about 4; 8 requests of 256K-1M
 // tokens (64 lists of 4K-16K pages, 153 MB) 37.5 us: scores 26 us at 5.9 TB/s, and
