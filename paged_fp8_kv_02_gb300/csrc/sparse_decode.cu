@@ -9,8 +9,9 @@
 //
 // One cluster of up to 8 CTAs per (request, KV head), four warps a CTA (eight where
 // there are few lists).  Each warp takes a contiguous run of the list's 16-token
-// tiles: its lanes look up 32 pages at a time (list, block table, scales: one chain of loads for all of
-// them), and a ring of TMA stages of its own keeps its K and V tiles in flight.
+// tiles: its lanes look up 32 pages at a time (list, block table, scales: one chain
+// of loads for all of them), and a ring of TMA stages of its own keeps its K and V
+// tiles in flight.
 // The warps' states (m, l, o) stay in shared memory and are joined by log-sum-exp
 // through distributed shared memory, so the whole step is one launch without
 // scratch in global memory.  Long lists are bounded by HBM; short ones by the
