@@ -197,6 +197,18 @@ def _want(name: str, t, dtype, shape, device: int) -> int:
                      f"{device}, got {t.dtype} {tuple(t.shape)} on {t.device}")
 
 
+def _count(name: str, v) -> int:
+    """A count for a 32-bit argument, which would be cut to its low bits otherwise."""
+    if -0x80000000 <= v <= 0x7FFFFFFF:
+        return int(v)
+    raise ValueError(f"{name}: {v} does not fit 32 bits")
+
+
+def _bound(v) -> int:
+    """An upper bound for a 32-bit argument: larger ones say no more than the largest."""
+    return _count("max_new_len", v if v <= 0x7FFFFFFF else 0x7FFFFFFF)
+
+
 def _on(device: int, f, *args):
     """f(*args) with `device` the current one."""
     import torch
@@ -246,7 +258,7 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, bloc
           _want("k_scales", k_scales, torch.float32, scales, dev), v[2],
           _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
           _want("context_lens", context_lens, torch.int32, (B,), dev),
-          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, T, int(max_new_len), H, D, P, pages)
+          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, T, _bound(max_new_len), H, D, P, pages)
 
 
 # ---------------------------------------------------------- block-sparse decode
@@ -267,7 +279,7 @@ def page_key_bounds(bounds, bound_scales, k_cache, block_tables, context_lens, n
           _want("k_cache", k_cache, torch.uint8, (pages, H, P, D), dev),
           _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
           _want("context_lens", context_lens, torch.int32, (B,), dev),
-          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, int(max_new_len), H, D, P, pages)
+          _want("new_start", new_start, torch.int32, (B + 1,), dev), B, _bound(max_new_len), H, D, P, pages)
 
 
 def select_pages_workspace_size(batch: int, num_kv_heads: int, max_pages_per_seq: int) -> int:
@@ -305,8 +317,9 @@ def select_pages(selected, q, bounds, bound_scales, block_tables, context_lens, 
           _want("bound_scales", bound_scales, torch.float32, (pages, Hkv), dev),
           None if k_scales is None else _want("k_scales", k_scales, torch.float32, (pages, Hkv), dev),
           _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
-          _want("context_lens", context_lens, torch.int32, (B,), dev), B, Hq, Hkv, D, int(page_size), pages, top,
-          int(sink_pages), int(recent_pages), None if workspace is None else _want("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes,
+          _want("context_lens", context_lens, torch.int32, (B,), dev), B, Hq, Hkv, D, _count("page_size", page_size), pages,
+          top, _count("sink_pages", sink_pages), _count("recent_pages", recent_pages),
+          None if workspace is None else _want("workspace", workspace, torch.uint8, (nbytes,), dev), nbytes,
           None if unit_status is None else _want("unit_status", unit_status, torch.int32, (B, Hkv), dev))
     return workspace
 

@@ -130,3 +130,50 @@ def test_select_sizes_its_workspace_on_the_tensors_device(monkeypatch, current):
                          T(torch.float32, 9, 4), T(torch.int32, 2, 9000), T(torch.int32, 2), 16)
     assert [c[:2] for c in calls] == [("size", 1), ("call", 1)] and state["device"] == current
     assert ws.numel() == 1024 and calls[0][2] == (2, 4, 9000) and calls[1][2][-1] == 78 and 1024 in calls[1][2]
+
+
+def test_counts_beyond_32_bits_are_not_cut(monkeypatch):
+    """A bound on the new tokens may be as large as one likes; other counts that
+    do not fit are refused.  ctypes alone would pass their low bits."""
+    import torch
+
+    import paged_fp8_kv_02_gb300 as pf
+    calls = {}
+
+    class Lib:
+        @staticmethod
+        def pfkv_kv_append_fp8_block(*args):
+            calls["append"] = args
+            return 0
+
+        @staticmethod
+        def pfkv_page_key_bounds(*args):
+            calls["bounds"] = args
+            return 0
+
+        @staticmethod
+        def pfkv_select_pages(*args):
+            calls["select"] = args
+            return 0
+
+    monkeypatch.setattr(pf, "_lib", Lib)
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    T = lambda dt, *s: FakeTensor(s, dt, 0)
+    x, cache, scales = T(torch.bfloat16, 5, 2, 128), T(torch.uint8, 9, 2, 16, 128), T(torch.float32, 9, 2)
+    bt, ctx, start = T(torch.int32, 3, 7), T(torch.int32, 3), T(torch.int32, 4)
+    bnd = T(torch.int8, 9, 2, 2, 128)
+    for given, passed in ((5, 5), (0, 0), (-3, -3), (2 ** 31 - 1, 2 ** 31 - 1), (2 ** 31, 2 ** 31 - 1), (2 ** 32, 2 ** 31 - 1),
+                          (2 ** 64 + 1, 2 ** 31 - 1)):
+        pf.kv_append_fp8_block(x, x, cache, cache, scales, scales, bt, ctx, start, given)
+        pf.page_key_bounds(bnd, scales, cache, bt, ctx, start, given)
+        assert calls["append"][12] == passed and calls["bounds"][8] == passed
+    select = lambda **kw: pf.select_pages(T(torch.int32, 3, 2, 4), T(torch.bfloat16, 3, 8, 128), bnd, scales, bt, ctx,
+                                          **{"page_size": 16, "workspace": T(torch.uint8, 512), **kw})
+    select()
+    assert calls["select"][12] == 16
+    for name in ("page_size", "sink_pages", "recent_pages"):
+        with pytest.raises(ValueError, match=name):
+            select(**{name: 2 ** 32 + 1})
+    with pytest.raises(ValueError, match="max_new_len"):
+        pf.page_key_bounds(bnd, scales, cache, bt, ctx, start, -2 ** 32)
