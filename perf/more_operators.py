@@ -223,7 +223,6 @@ def prepare(case, seed):
     counts = _counts(case)
     rows = sum(counts)
     s["q_start"] = torch.from_numpy(np.concatenate([[0], np.cumsum(counts)]).astype(np.int32)).cuda()
-    s["max_q_len"] = max(counts)
     s["target"] = torch.empty((rows, vocab), dtype=dtype, device="cuda")
     s["draft"] = torch.empty((rows, vocab), dtype=dtype, device="cuda") if case["draft"] else None
     tokens = torch.zeros(rows, dtype=torch.int64, device="cuda")
@@ -370,8 +369,7 @@ def run(state):
             s["arrays"] = pf.PagedArrays([layer for x in _arrays(s) for layer in x])
         pf.copy_pages(s["arrays"], s["pairs"])
         return _copy_outputs(s)
-    pf.verify_drafts(s["next_tokens"], s["accepted"], s["target"], s["draft"], s["tokens"], s["uniforms"], s["q_start"],
-                     s["max_q_len"])
+    pf.verify_drafts(s["next_tokens"], s["accepted"], s["target"], s["draft"], s["tokens"], s["uniforms"], s["q_start"])
     return {"next": s["next_tokens"], "accepted": s["accepted"]}
 
 
