@@ -198,6 +198,76 @@ PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void
                                       pfkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* Rotary positions.  The pages have no counterpart of these calls: they are
+ * the step between a layer's projections and the append.
+ *
+ * Pair i of a row's channels turns by the angle phi = position * frequency_i,
+ * where the position is the token's on the pair's axis a_i (one axis for text;
+ * time, height and width for pictures and video):
+ *     x' = x cos(phi) - y sin(phi),   y' = y cos(phi) + x sin(phi)
+ * The pair is (first + i, first + num_pairs + i), or (first + 2i, first + 2i + 1)
+ * where `neighbours` is set; channels outside [first, first + 2 num_pairs) stay.
+ * A frequency is kept as the fraction of a turn per position in units of 2^-64,
+ * so position times frequency wraps exactly in 64-bit integers: a far position
+ * costs no more than the frequency's own rounding to double (2^-52 of the angle),
+ * and a negative one turns back.  The fraction's upper 32 bits, rounded to fp32,
+ * give sine and cosine (angle off by at most 2^-24 rad); pairs turn in fp32 and
+ * are rounded once. */
+#define PFKV_ROTARY_MAX_PAIRS 128
+#define PFKV_ROTARY_MAX_AXES 8
+/* Host description of a model's rotary positions, filled by pfkv_rotary_init
+ * and passed by address; a call copies it (a captured launch keeps its copy). */
+typedef struct {
+  int32_t first, num_pairs, neighbours, num_axes;
+  uint64_t turns[PFKV_ROTARY_MAX_PAIRS];
+  uint8_t axis[PFKV_ROTARY_MAX_PAIRS];
+} pfkv_rotary;
+/* frequencies: host, radians per position, finite (scaled ones are given
+ * scaled); axes: host, the axis of each pair in [0, num_axes), or NULL (all 0).
+ * num_pairs a multiple of 8 up to 128, first a multiple of 16, num_axes 1..8. */
+PFKV_API int pfkv_rotary_init(pfkv_rotary *rotary, const double *frequencies, const int32_t *axes,
+                              int num_pairs, int num_axes, int first, int neighbours);
+
+/* rotary_embed -- rows of bf16 turned by their token's positions.
+ *   out, x      bf16 [num_tokens][num_heads][head_dim]; the elements between two
+ *               tokens are the strides (multiples of 8, at least num_heads *
+ *               head_dim, below 2^31), so that both may be parts of wider rows.  out == x
+ *               with the same stride turns in place (only the turning channels
+ *               are written); other overlaps are an error.
+ *   positions   int32 [num_axes][num_tokens]
+ * For caches that rotary_append_fp8 does not fill: turned keys go on to
+ * kv_append_fp8_block or kv_append_bf16.  Supported: head_dim a multiple of 16
+ * up to 4096 with first + 2 num_pairs <= head_dim. */
+PFKV_API int pfkv_rotary_embed(void *out, int64_t out_stride, const void *x, int64_t x_stride,
+                               const int32_t *positions, const pfkv_rotary *rotary, int num_tokens,
+                               int num_heads, int head_dim, pfkv_stream_t stream);
+
+/* rotary_append_fp8 -- rotary_embed of the queries, and of the new keys on
+ * their way through kv_append_fp8_scaled, in one launch: a key turns in fp32
+ * and is rounded once, to its e4m3 code.  Values do not turn; their codes and
+ * scales are those of kv_append_fp8_scaled.
+ *   q_out, q    as out, x of rotary_embed with num_q_heads; both NULL: keys and
+ *               values only (num_q_heads is then ignored)
+ *   k_new, v_new  bf16 [num_tokens][num_kv_heads][head_dim] with token strides
+ *               like q's; v_new = v_cache = v_scales = NULL: keys only (an MLA
+ *               latent: num_kv_heads 1, the last channels turn)
+ *   slot_mapping  int64 [num_tokens]; a token whose slot is < 0 or outside the
+ *               cache is not appended; its query turns all the same
+ *   granularity TENSOR, HEAD: scales are read.  TOKEN: written; the largest
+ *               magnitude is taken after the turn (head_dim <= 512).  BLOCK:
+ *               an error (rotary_embed, then kv_append_fp8_block).
+ * q_out must not overlap k_new or v_new.  Other arguments, layouts, support and
+ * errors as kv_append_fp8_scaled and rotary_embed. */
+PFKV_API int pfkv_rotary_append_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
+                                    const void *k_new, int64_t k_stride, const void *v_new,
+                                    int64_t v_stride, void *k_cache, void *v_cache,
+                                    const int64_t *slot_mapping, const int32_t *positions,
+                                    const pfkv_rotary *rotary, int num_tokens, int num_q_heads,
+                                    int num_kv_heads, int head_dim, int page_size, int64_t num_pages,
+                                    pfkv_scale_granularity granularity, float *k_scales,
+                                    float *v_scales, pfkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* paged_decode_attn -- one decode step of GQA/MHA attention over the paged
  * cache, dequantising on read, with split-KV and a log-sum-exp merge.
  *
@@ -495,6 +565,61 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
                                      float *lse_out, pfkv_stream_t stream);
 
 /* ------------------------------------------------------------------------ */
+/* verify_drafts -- which drafted tokens stay, after a verification pass.
+ *
+ * Explainer, "Speculative Decoding" section: the target model checks the
+ * drafted positions in one forward pass (pfkv_paged_prefill_attn) and the
+ * longest accepted run stays.  The rule is the published one of speculative
+ * sampling (Leviathan et al. 2023): the tokens that come out are distributed as
+ * the target's own.
+ *
+ * Request b's query tokens are rows q_start[b] .. q_start[b+1] - 1 of the pass:
+ * its last known token, then n_b - 1 drafted ones.  With p_i and q_i the
+ * target's and the draft's distribution of the token AFTER row i, u_i its
+ * random number and x_i = tokens[i+1], going through the request's rows:
+ *     x_i stays while  u_i q_i(x_i) < p_i(x_i)      (the product is exact)
+ * At the first row r where it does not, the next token is drawn with weights
+ * max(p_r - q_r, 0) (one fp32 subtraction); where all stay, with p_r of the
+ * last row.  Drawing: w(t) = floor(2^42 min(weight, 1)) as 64-bit integers, U =
+ * floor(2^24 u) of the request's LAST row, W = sum w; the token is the smallest
+ * t with w(0) + .. + w(t) > floor(W U / 2^24).  Integers make the result the
+ * same in any order of summation.  If W is 0 the weights p_r are taken.
+ *   next_tokens    int32 [num_tokens], written: row i's following token: the
+ *                  accepted x_i, then the drawn one, then -1
+ *   accepted       int32 [batch], written: drafted tokens that stay
+ *   target_probs   [num_tokens][vocab_size] of prob_dtype, rows target_stride
+ *                  elements apart (>= vocab_size)
+ *   draft_probs    likewise; the last row of a request is not read.  NULL: the
+ *                  drafts were not sampled (looked up in the prompt, or greedy),
+ *                  q_i is 1 at x_i and 0 elsewhere
+ *   tokens         int32 [num_tokens]; uniforms fp32 [num_tokens] in [0, 1)
+ *   q_start        int32 [batch + 1] (device), as paged_prefill_attn's
+ *   context_lens   optional int32 [batch], read and written: L_b (which counted
+ *                  all drafts) loses the rejected ones, n_b - 1 - accepted[b]
+ *   request_status optional int32 [batch], written: 0 or an OR of
+ *     PFKV_REQ_BAD_INDEX  q_start of this request decreases or leaves [0,
+ *                         num_tokens]: accepted is 0 and no row is written
+ *     PFKV_REQ_BAD_TOKEN  a drafted token that was looked at is outside the
+ *                         vocabulary: it does not stay
+ *     PFKV_REQ_NO_MASS    neither weights have mass: the drawn token is -1
+ * A request without rows has accepted 0.  Rows that a broken q_start gives to two
+ * requests are written by both.  Probabilities that are NaN or negative
+ * count as 0 in weights, and NaN never accepts.  Nothing waits for the host: the
+ * call can be captured, and the rows of K/V behind the new length are
+ * overwritten by the next append.
+ * Supported: vocab_size up to 2^20; rows need no alignment beyond their type's
+ * (16-byte aligned rows are read in wider loads). */
+#define PFKV_REQ_BAD_TOKEN 0x4
+#define PFKV_REQ_NO_MASS 0x8
+typedef enum { PFKV_PROB_F32 = 0, PFKV_PROB_BF16 = 1, PFKV_PROB_F16 = 2 } pfkv_prob_dtype;
+PFKV_API int pfkv_verify_drafts(int32_t *next_tokens, int32_t *accepted, const void *target_probs,
+                                int64_t target_stride, const void *draft_probs, int64_t draft_stride,
+                                pfkv_prob_dtype prob_dtype, const int32_t *tokens,
+                                const float *uniforms, const int32_t *q_start, int batch,
+                                int num_tokens, int vocab_size, int32_t *context_lens,
+                                int32_t *request_status, pfkv_stream_t stream);
+
+/* ------------------------------------------------------------------------ */
 /* mla_decode_attn -- MLA absorbed-latent decode over one shared e4m3 latent
  * row per token, optionally restricted to a top-k token list.
  *
@@ -628,12 +753,75 @@ PFKV_API int pfkv_pool_map_request(pfkv_page_pool *pool, const int32_t *tokens, 
  * free list.  PFKV_ERR_INVALID_ARG (nothing changed) if an entry is not a held
  * page, or lists a page more times than it has holders. */
 PFKV_API int pfkv_pool_release(pfkv_page_pool *pool, const int32_t *block_table_row, int n_pages);
+/* Add a holder to each of a request's first n_pages pages: a fork, which
+ * shares them all (release each of the two rows once).  PFKV_ERR_INVALID_ARG
+ * (nothing changed) if an entry is not a held page. */
+PFKV_API int pfkv_pool_fork(pfkv_page_pool *pool, const int32_t *block_table_row, int n_pages);
+/* Bring a request to ceil(n_tokens / page_size) pages: fresh pages behind its
+ * last one (a context that grows), or its last ones released (rejected drafts,
+ * a conversation cut short).  The row's leading entries >= 0 are its pages;
+ * entries that change are written (-1 and tag 0 past the last).
+ * PFKV_ERR_NO_PAGES or PFKV_ERR_INVALID_ARG (a row of max_pages entries that is
+ * too short, an entry that is not held): nothing changed. */
+PFKV_API int pfkv_pool_resize(pfkv_page_pool *pool, int32_t *block_table_row, uint32_t *table_tags,
+                              int max_pages, int n_tokens);
+/* Before a request writes rows of token first_token and later ones into pages
+ * that others may share, or that are known by the hash of other tokens (after
+ * a fork or a cut): each of its pages from first_token / page_size on that has
+ * other holders is given up for a fresh one, and pages it holds alone leave the
+ * prefix table.  Where the first of them keeps earlier rows (first_token is
+ * not a multiple of page_size), pair[0], pair[1] = old, new page and *n_pairs =
+ * 1: copy the page (pfkv_copy_pages) before the next holder writes to either;
+ * otherwise *n_pairs = 0.  Row and tags are written where pages change.
+ * PFKV_ERR_NO_PAGES, PFKV_ERR_INVALID_ARG: nothing changed. */
+PFKV_API int pfkv_pool_make_writable(pfkv_page_pool *pool, int32_t *block_table_row,
+                                     uint32_t *table_tags, int max_pages, int first_token,
+                                     int32_t *pair, int *n_pairs);
+/* Move held pages from the highest ids to the lowest free ones, max_moves at
+ * most, so that the pool's end can be given back.  pairs[k] = (old, new) page
+ * of move k (the pages are distinct: copy them in any order, with one
+ * pfkv_copy_pages); remap[num_pages] = the new id of every page.  Holders,
+ * prefix entries and fresh tags move along; the caller rewrites its rows
+ * (row[i] = remap[row[i]]) and their tags (pfkv_pool_page_tags).  Free pages
+ * are handed out lowest id first afterwards. */
+PFKV_API int pfkv_pool_compact(pfkv_page_pool *pool, int64_t max_moves, int32_t *pairs,
+                               int32_t *remap, int64_t *n_moves);
 /* The FNV-1a chain hash of one block (n tokens) given its parent's hash. */
 PFKV_API uint64_t pfkv_block_hash(uint64_t parent, const int32_t *tokens, int n);
 /* slots_out[k] = page * page_size + t % page_size for tokens t = first_token +
  * k of a request (host arrays): the slot mapping kv_append_fp8 takes. */
 PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages, int page_size,
                                    int first_token, int n_tokens, int64_t *slots_out);
+
+/* ------------------------------------------------------------------------ */
+/* copy_pages -- pages copied within caches, in one launch for all layers: what
+ * a fork's first write (pfkv_pool_make_writable) and a compaction
+ * (pfkv_pool_compact) need.  KV cache explainer, "PagedAttention の 2 つの原語":
+ * pages are shared, and copied when a holder writes.
+ * For every pair (s, d) and every array: page d becomes a copy of page s.
+ *   arrays       host array of num_arrays descriptions (read during the call):
+ *                K, V, scales, bounds, latents of any number of layers, each
+ *                num_pages pages of page_bytes bytes, page_stride bytes apart
+ *                (>= page_bytes)
+ *   pairs        int32 [num_pairs][2] (device): source, destination.  A pair
+ *                with a negative entry is padding.
+ *   pair_status  optional int32 [num_pairs], written: 0, or PFKV_DEVERR_BAD_PAGE
+ *                for a pair that names a page >= num_pages (not copied)
+ * A page may be the source of many pairs.  A page that is the destination of
+ * two pairs, or the destination of one and the source of another, ends with
+ * unspecified bytes of the pages involved (the copies run at the same time);
+ * the pool calls give no such pairs in one list unless pages are released
+ * between the calls that make the list.
+ * Any alignment and size; pages and strides that are multiples of 16 bytes are
+ * the fast ones.  Supported: page_bytes < 2^31; arrays beyond 128 take another
+ * launch each 128. */
+typedef struct {
+  void *base;
+  int64_t page_bytes, page_stride;
+} pfkv_paged_array;
+PFKV_API int pfkv_copy_pages(const pfkv_paged_array *arrays, int num_arrays, const int32_t *pairs,
+                             int num_pairs, int64_t num_pages, int32_t *pair_status,
+                             pfkv_stream_t stream);
 
 /* Copy the workspace status word (bits PFKV_DEVERR_*) to *status after
  * synchronising `stream`.  Returns PFKV_OK, or PFKV_ERR_CUDA. */

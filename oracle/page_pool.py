@@ -100,3 +100,87 @@ class PagePool:
                 if h is not None and self.prefix.get(h) == page:
                     del self.prefix[h]
                 self.free.append(page)
+
+    # ------------------------------------------------- a request that changes
+    def _held(self, row):
+        """The row's leading pages, each listed no more often than it is held."""
+        pages = []
+        for page in row:
+            if page < 0:
+                break
+            pages.append(page)
+        for page in set(pages):
+            if page >= len(self.ref) or self.ref[page] < pages.count(page):
+                raise ValueError("not a held page")
+        return pages
+
+    def _fresh(self):
+        page = self.free.pop()
+        self.ref[page] = 1
+        self.tag[page] += 1
+        return page
+
+    def _forget(self, page):
+        h = self.hash_of.pop(page, None)
+        if h is not None and self.prefix.get(h) == page:
+            del self.prefix[h]
+
+    def fork(self, row, n_pages: int):
+        for page in row[:n_pages]:
+            if page < 0 or page >= len(self.ref) or self.ref[page] <= 0:
+                raise ValueError("not a held page")
+        for page in row[:n_pages]:
+            self.ref[page] += 1
+
+    def resize(self, row, tags, n_tokens: int):
+        pages = self._held(row)
+        want = -(-n_tokens // self.page_size)
+        if want > len(row):
+            raise ValueError("row too short")
+        if want - len(pages) > len(self.free):
+            raise NoPages
+        for i in range(len(pages), want):
+            row[i] = self._fresh()
+            tags[i] = self.tag[row[i]]
+        for i in range(want, len(pages)):
+            self.release([row[i]], 1)
+            row[i], tags[i] = -1, 0
+
+    def make_writable(self, row, tags, first_token: int):
+        """-> [(old page, new page)] to copy, one pair at most."""
+        pages = self._held(row)
+        first = first_token // self.page_size
+        if sum(self.ref[p] > 1 for p in pages[first:]) > len(self.free):
+            raise NoPages
+        pairs = []
+        for i in range(first, len(pages)):
+            old = pages[i]
+            if self.ref[old] == 1:
+                self._forget(old)
+                continue
+            row[i] = self._fresh()
+            tags[i] = self.tag[row[i]]
+            self.ref[old] -= 1
+            if i * self.page_size < first_token:
+                pairs.append((old, row[i]))
+        return pairs
+
+    def compact(self, max_moves: int):
+        pairs = []
+        while len(pairs) < max_moves:
+            free = min((p for p, r in enumerate(self.ref) if r == 0), default=None)
+            held = max((p for p, r in enumerate(self.ref) if r > 0), default=None)
+            if free is None or held is None or free > held:
+                break
+            self.ref[free], self.ref[held] = self.ref[held], 0
+            self.tag[free] += 1
+            if held in self.hash_of:
+                h = self.hash_of.pop(held)
+                self.hash_of[free] = h
+                self.prefix[h] = free
+            pairs.append((held, free))
+        self.free = sorted((p for p, r in enumerate(self.ref) if r == 0), reverse=True)
+        remap = list(range(len(self.ref)))
+        for old, new in pairs:
+            remap[old] = new
+        return pairs, remap

@@ -23,11 +23,13 @@ __all__ = [
     "paged_sparse_decode_attn",
     "paged_decode_workspace_size", "paged_decode_attn", "paged_decode_attn_noalloc", "paged_decode_attn_scaled",
     "paged_prefill_workspace_size", "paged_prefill_attn",
+    "Rotary", "rotary_embed", "rotary_append_fp8", "verify_drafts", "PagedArrays", "copy_pages",
     "SCALE_TENSOR", "SCALE_HEAD", "SCALE_TOKEN", "SCALE_BLOCK",
     "mla_decode_workspace_size",
     "mla_decode_attn", "validate_tables", "verify_page_tags", "workspace_status", "selftest_barrier_timeout",
     "last_error", "version",
     "CACHE_FP8_E4M3", "CACHE_BF16", "DEVERR", "REQ_TAG_MISMATCH", "REQ_BAD_INDEX",
+    "REQ_BAD_TOKEN", "REQ_NO_MASS",
     "PagePool", "block_hash", "slots_from_table",
 ]
 
@@ -39,7 +41,9 @@ DEVERR = {
 }
 
 REQ_TAG_MISMATCH = 0x1  # verify_page_tags: a page the request reads carries another tag
-REQ_BAD_INDEX = 0x2     # verify_page_tags: a page id or context length out of range
+REQ_BAD_INDEX = 0x2     # verify_page_tags: a page id or context length out of range; verify_drafts: q_start
+REQ_BAD_TOKEN = 0x4     # verify_drafts: a drafted token outside the vocabulary
+REQ_NO_MASS = 0x8       # verify_drafts: no weight to draw a token with
 
 _lock = threading.Lock()
 _lib = None
@@ -75,6 +79,12 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
                                                 vp]),
             "pfkv_kv_append_fp8_block": (i32, [vp, vp, vp, vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32,
                                                i32, i64, vp]),
+            "pfkv_rotary_init": (i32, [vp, vp, vp, i32, i32, i32, i32]),
+            "pfkv_rotary_embed": (i32, [vp, i64, vp, i64, vp, vp, i32, i32, i32, vp]),
+            "pfkv_rotary_append_fp8": (i32, [vp, i64, vp, i64, vp, i64, vp, i64, vp, vp, vp, vp, vp, i32, i32, i32,
+                                             i32, i32, i64, i32, vp, vp, vp]),
+            "pfkv_verify_drafts": (i32, [vp, vp, vp, i64, vp, i64, i32, vp, vp, vp, i32, i32, i32, vp, vp, vp]),
+            "pfkv_copy_pages": (i32, [vp, i32, vp, i32, i64, vp, vp]),
             "pfkv_page_key_bounds": (i32, [vp, vp, vp, vp, i32, vp, vp, i32, i32, i32, i32, i32, i64, vp]),
             "pfkv_select_pages_workspace_size": (sz, [i32, i32, i32]),
             "pfkv_select_pages": (i32, [vp, vp, vp, vp, vp, vp, i32, vp, i32, i32, i32, i32, i32, i64, i32, i32,
@@ -104,6 +114,10 @@ def load(build_if_missing: bool = True) -> ctypes.CDLL:
             "pfkv_pool_page_tags": (i32, [vp, vp]),
             "pfkv_pool_map_request": (i32, [vp, vp, i32, vp, vp, i32, vp]),
             "pfkv_pool_release": (i32, [vp, vp, i32]),
+            "pfkv_pool_fork": (i32, [vp, vp, i32]),
+            "pfkv_pool_resize": (i32, [vp, vp, vp, i32, i32]),
+            "pfkv_pool_make_writable": (i32, [vp, vp, vp, i32, i32, vp, vp]),
+            "pfkv_pool_compact": (i32, [vp, i64, vp, vp, vp]),
             "pfkv_block_hash": (ctypes.c_uint64, [ctypes.c_uint64, vp, i32]),
             "pfkv_slots_from_table": (i32, [vp, i32, i32, i32, i32, vp]),
             "pfkv_selftest_barrier_timeout": (i32, [vp, vp]),
@@ -259,6 +273,108 @@ def kv_append_fp8_block(k_new, v_new, k_cache, v_cache, k_scales, v_scales, bloc
           _want("block_tables", block_tables, torch.int32, (B, maxp), dev), maxp,
           _want("context_lens", context_lens, torch.int32, (B,), dev),
           _want("new_start", new_start, torch.int32, (B + 1,), dev), B, T, _bound(max_new_len), H, D, P, pages)
+
+
+# ------------------------------------------------------------ rotary positions
+class _RotaryStruct(ctypes.Structure):
+    _fields_ = [("first", ctypes.c_int32), ("num_pairs", ctypes.c_int32), ("neighbours", ctypes.c_int32),
+                ("num_axes", ctypes.c_int32), ("turns", ctypes.c_uint64 * 128), ("axis", ctypes.c_uint8 * 128)]
+
+
+class Rotary:
+    """A model's rotary positions (``pfkv_rotary_init``), on the host: pair i
+    turns by frequencies[i] radians per position on axis axes[i] (None: one
+    axis).  The pairs are channels (first + i, first + n + i), or with
+    ``neighbours`` (first + 2i, first + 2i + 1).  num_axes: rows of the
+    positions, by default one more than the largest axis named."""
+
+    def __init__(self, frequencies, axes=None, first: int = 0, neighbours: bool = False, num_axes: int = None):
+        import numpy as np
+        f, fp = _host(frequencies, np.float64)
+        if f.ndim != 1:
+            raise ValueError("frequencies: expected one number per pair")
+        ap = None
+        if axes is not None:
+            x = np.asarray(axes)
+            if x.shape != f.shape or not np.issubdtype(x.dtype, np.integer):
+                raise ValueError("axes: expected one whole number per pair")
+            if x.size and not (0 <= x.min() and x.max() < 128):
+                raise ValueError("axes: out of range")
+            x, ap = _host(x, np.int32)
+            if num_axes is None and x.size:
+                num_axes = int(x.max()) + 1
+        self._struct = _RotaryStruct()
+        self.num_axes = 1 if num_axes is None else _count("num_axes", num_axes)
+        _check("rotary_init", load().pfkv_rotary_init(ctypes.byref(self._struct), fp, ap, f.shape[0], self.num_axes,
+                                                      _count("first", first), 1 if neighbours else 0))
+        self._ptr = ctypes.addressof(self._struct)
+
+
+def _rows(name: str, t, dtype, shape, device: int):
+    """Address of a tensor [tokens][...] and the elements between two tokens;
+    what belongs to one token is contiguous.  ValueError otherwise."""
+    if t.dtype is dtype and t.shape == shape and t.get_device() == device:
+        if t.is_contiguous():
+            row = 1
+            for n in shape[1:]:
+                row *= n
+            return t.data_ptr(), row
+        if shape[0] <= 1 or t[0].is_contiguous():
+            return t.data_ptr(), t.stride(0)
+    raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on the call's device {device}, "
+                     f"contiguous within a token, got {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
+
+
+def _positions(t, rotary: Rotary, tokens: int, device: int) -> int:
+    import torch
+    shape = (tokens,) if rotary.num_axes == 1 and t.dim() == 1 else (rotary.num_axes, tokens)
+    return _want("positions", t, torch.int32, shape, device)
+
+
+def rotary_embed(out, x, positions, rotary: Rotary, stream=None):
+    """Turn bf16 rows x [T][H][D] by their token's positions int32 [axes][T]
+    ([T] for one axis) into out, which may be x itself.  Both may be parts of
+    wider rows (any stride between tokens that is a multiple of 8)."""
+    import torch
+    dev = x.get_device()
+    T, H, D = x.shape
+    o, os = _rows("out", out, torch.bfloat16, (T, H, D), dev)
+    i, is_ = _rows("x", x, torch.bfloat16, (T, H, D), dev)
+    _call("rotary_embed", dev, stream, o, os, i, is_, _positions(positions, rotary, T, dev), rotary._ptr, T, H, D)
+
+
+def rotary_append_fp8(q_out, q, k_new, v_new, k_cache, v_cache, slot_mapping, positions, rotary: Rotary,
+                      granularity: int, k_scales, v_scales=None, stream=None):
+    """rotary_embed of the queries q [T][Hq][D] into q_out and of the keys k_new
+    [T][H][D] on their way through kv_append_fp8_scaled, with v_new, in one
+    launch: caches uint8 [pages][H][P][D], slot_mapping int64 [T]; SCALE_TENSOR
+    [1] / SCALE_HEAD [H] are read, SCALE_TOKEN [pages][H][P] is written.  q_out
+    = q = None: no queries.  v_new = v_cache = v_scales = None: keys only."""
+    import torch
+    dev = k_new.get_device()
+    T, H, D = k_new.shape
+    pages, _, P, _ = k_cache.shape
+    cache, dt = (pages, H, P, D), torch.bfloat16
+    scales = {SCALE_TENSOR: (1,), SCALE_HEAD: (H,), SCALE_TOKEN: (pages, H, P)}.get(granularity, k_scales.shape)
+    o = os = i = is_ = Hq = 0
+    if q is not None or q_out is not None:
+        if q is None or q_out is None:
+            raise ValueError("q_out and q: both or none")
+        Hq = q.shape[1]
+        o, os = _rows("q_out", q_out, dt, (T, Hq, D), dev)
+        i, is_ = _rows("q", q, dt, (T, Hq, D), dev)
+    k, ks = _rows("k_new", k_new, dt, (T, H, D), dev)
+    v = vs = vc = vsc = 0
+    if not (v_new is None and v_cache is None and v_scales is None):
+        if v_new is None or v_cache is None or v_scales is None:
+            raise ValueError("v_new, v_cache and v_scales: all or none")
+        v, vs = _rows("v_new", v_new, dt, (T, H, D), dev)
+        vc = _want("v_cache", v_cache, torch.uint8, cache, dev)
+        vsc = _want("v_scales", v_scales, torch.float32, scales, dev)
+    _call("rotary_append_fp8", dev, stream, o, os, i, is_, k, ks, v, vs,
+          _want("k_cache", k_cache, torch.uint8, cache, dev), vc,
+          _want("slot_mapping", slot_mapping, torch.int64, (T,), dev), _positions(positions, rotary, T, dev), rotary._ptr,
+          T, Hq, H, D, P, pages, int(granularity), _want("k_scales", k_scales, torch.float32, scales, dev), vsc)
 
 
 # ---------------------------------------------------------- block-sparse decode
@@ -454,6 +570,36 @@ def paged_prefill_attn(out, q, k_cache, v_cache, block_tables, context_lens, q_s
     return workspace
 
 
+def verify_drafts(next_tokens, accepted, target_probs, draft_probs, tokens, uniforms, q_start, context_lens=None,
+                  request_status=None, stream=None):
+    """Which drafted tokens stay after a verification pass over the rows
+    q_start int32 [B+1] (a request's last known token, then its drafts):
+    next_tokens int32 [T] receives the token that follows each row (accepted
+    ones, a drawn one, then -1) and accepted int32 [B] their number.
+    target_probs float32, bfloat16 or float16 [T][V] is the target's
+    distribution of the token after each row; draft_probs likewise the draft's,
+    or None where drafts were not sampled; tokens int32 [T]; uniforms float32
+    [T] in [0, 1).  Rows of probabilities may lie further apart than V.
+    context_lens: optional int32 [B] that loses the rejected tokens;
+    request_status: optional int32 [B]."""
+    import torch
+    dev = target_probs.get_device()
+    T, V = target_probs.shape
+    B = q_start.shape[0] - 1
+    dt = target_probs.dtype
+    kind = {torch.float32: 0, torch.bfloat16: 1, torch.float16: 2}.get(dt)
+    if kind is None:
+        raise ValueError(f"target_probs: expected float32, bfloat16 or float16, got {dt}")
+    p, ps = _rows("target_probs", target_probs, dt, (T, V), dev)
+    q, qs = (None, 0) if draft_probs is None else _rows("draft_probs", draft_probs, dt, (T, V), dev)
+    i32 = torch.int32
+    _call("verify_drafts", dev, stream, _want("next_tokens", next_tokens, i32, (T,), dev),
+          _want("accepted", accepted, i32, (B,), dev), p, ps, q, qs, kind, _want("tokens", tokens, i32, (T,), dev),
+          _want("uniforms", uniforms, torch.float32, (T,), dev), _want("q_start", q_start, i32, (B + 1,), dev), B, T, V,
+          None if context_lens is None else _want("context_lens", context_lens, i32, (B,), dev),
+          None if request_status is None else _want("request_status", request_status, i32, (B,), dev))
+
+
 def mla_decode_workspace_size(batch: int, num_heads: int, d_latent: int = 512, topk: int = 0) -> int:
     return int(load().pfkv_mla_decode_workspace_size(batch, num_heads, d_latent, topk))
 
@@ -515,6 +661,47 @@ def workspace_status(workspace, stream=None) -> int:
     return int(v.value)
 
 
+# ----------------------------------------------------------------- page copies
+class _PagedArrayStruct(ctypes.Structure):
+    _fields_ = [("base", ctypes.c_void_p), ("page_bytes", ctypes.c_int64), ("page_stride", ctypes.c_int64)]
+
+
+class PagedArrays:
+    """The tensors that hold a cache's pages, in all layers: K, V, scales,
+    bounds, latents, each [pages][...] with what belongs to a page contiguous.
+    Described once, for copy_pages; the tensors are kept."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        if not self.tensors:
+            raise ValueError("no tensors")
+        self.device = self.tensors[0].get_device()
+        self.num_pages = self.tensors[0].shape[0]
+        self._arrays = (_PagedArrayStruct * len(self.tensors))()
+        for k, t in enumerate(self.tensors):
+            if not t.is_cuda or t.get_device() != self.device:
+                raise ValueError(f"tensor {k}: on {t.device}, the first one on device {self.device}")
+            if t.dim() < 1 or t.shape[0] != self.num_pages or t.numel() == 0 or not t[0].is_contiguous():
+                raise ValueError(f"tensor {k}: expected [{self.num_pages}][...], contiguous within a page, got "
+                                 f"{tuple(t.shape)} with strides {tuple(t.stride())}")
+            size = t.element_size()
+            page = t[0].numel() * size
+            self._arrays[k] = _PagedArrayStruct(t.data_ptr(), page, t.stride(0) * size if self.num_pages > 1 else page)
+        self._ptr = ctypes.addressof(self._arrays)
+
+
+def copy_pages(arrays: PagedArrays, pairs, pair_status=None, stream=None):
+    """Copy page pairs[i][0] to page pairs[i][1] in every array (pairs int32
+    [n][2]; a pair with a negative entry is padding).  No page may be the
+    destination of two pairs, or of one and the source of another: its bytes
+    are unspecified then.  pair_status: optional int32 [n]."""
+    import torch
+    dev = arrays.device
+    n = pairs.shape[0]
+    _call("copy_pages", dev, stream, arrays._ptr, len(arrays.tensors), _want("pairs", pairs, torch.int32, (n, 2), dev), n,
+          arrays.num_pages, None if pair_status is None else _want("pair_status", pair_status, torch.int32, (n,), dev))
+
+
 # ------------------------------------------------------ page pool (host side)
 def _host(a, dtype):
     import numpy as np
@@ -573,6 +760,54 @@ class PagePool:
         if not 0 <= n_pages <= r.shape[0]:
             raise ValueError(f"n_pages {n_pages} outside the row's {r.shape[0]} entries")
         _check("pool_release", load().pfkv_pool_release(self._h, rp, n_pages))
+
+    def fork(self, row, n_pages: int):
+        """One more holder for each of the row's first n_pages pages."""
+        import numpy as np
+        r, rp = _host(row, np.int32)
+        if not 0 <= n_pages <= r.shape[0]:
+            raise ValueError(f"n_pages {n_pages} outside the row's {r.shape[0]} entries")
+        _check("pool_fork", load().pfkv_pool_fork(self._h, rp, n_pages))
+
+    @staticmethod
+    def _row(row, tags):
+        """Addresses of a row and its tags, which the call changes in place."""
+        import numpy as np
+        for name, a, dtype in (("row", row, np.int32), ("tags", tags, np.uint32)):
+            if not isinstance(a, np.ndarray) or a.dtype != dtype or a.ndim != 1 or not a.flags.c_contiguous or not a.flags.writeable:
+                raise ValueError(f"{name}: expected a writable contiguous {np.dtype(dtype)} array, which is changed in place")
+        if row.shape != tags.shape:
+            raise ValueError("row and tags: expected the same length")
+        return row.ctypes.data_as(ctypes.c_void_p), tags.ctypes.data_as(ctypes.c_void_p), row.shape[0]
+
+    def resize(self, row, tags, n_tokens: int):
+        """Grow or cut a request (row and tags of map_request, changed in
+        place) to the pages of n_tokens tokens."""
+        rp, tp, n = self._row(row, tags)
+        _check("pool_resize", load().pfkv_pool_resize(self._h, rp, tp, n, _count("n_tokens", n_tokens)))
+
+    def make_writable(self, row, tags, first_token: int):
+        """Give a request (row and tags changed in place) pages of its own from
+        token first_token on -> int32 [0 or 1][2], the page to copy before it
+        is written (copy_pages)."""
+        import numpy as np
+        rp, tp, n = self._row(row, tags)
+        pair, k = np.zeros((1, 2), np.int32), ctypes.c_int(0)
+        _check("pool_make_writable", load().pfkv_pool_make_writable(
+            self._h, rp, tp, n, _count("first_token", first_token), pair.ctypes.data_as(ctypes.c_void_p), ctypes.byref(k)))
+        return pair[:k.value]
+
+    def compact(self, max_moves: int = None):
+        """Move held pages to the lowest free ids -> (int32 [n][2] pages to copy,
+        int32 [num_pages] new id of every page).  The holders' rows follow:
+        row[row >= 0] = remap[row[row >= 0]], tags from page_tags()."""
+        import numpy as np
+        most = self.num_pages if max_moves is None else min(max_moves, self.num_pages)
+        pairs, remap = np.zeros((max(most, 0), 2), np.int32), np.zeros(self.num_pages, np.int32)
+        k = ctypes.c_int64(0)
+        _check("pool_compact", load().pfkv_pool_compact(self._h, most, pairs.ctypes.data_as(ctypes.c_void_p),
+                                                        remap.ctypes.data_as(ctypes.c_void_p), ctypes.byref(k)))
+        return pairs[:k.value].copy(), remap
 
 
 def block_hash(parent: int, tokens) -> int:

@@ -73,14 +73,32 @@ int32_t take_page(pfkv_page_pool* p) {
   return page;
 }
 
+void leave_prefix(pfkv_page_pool* p, int32_t page) {
+  if (!p->registered[page]) return;
+  auto it = p->prefix.find(p->page_hash[page]);
+  if (it != p->prefix.end() && it->second == page) p->prefix.erase(it);
+  p->registered[page] = 0;
+}
+
 void drop_ref(pfkv_page_pool* p, int32_t page) {
   if (--p->refcount[page] > 0) return;
-  if (p->registered[page]) {
-    auto it = p->prefix.find(p->page_hash[page]);
-    if (it != p->prefix.end() && it->second == page) p->prefix.erase(it);
-    p->registered[page] = 0;
-  }
+  leave_prefix(p, page);
   p->free_list.push_back(page);
+}
+
+// Pages of a row: its leading entries >= 0.  -1 with *bad set where one of them
+// is not held, or is listed more often than it has holders.
+int held_pages(pfkv_page_pool* p, const int32_t* row, int max_pages, int32_t* bad) {
+  int n = 0, ok = 0;
+  while (n < max_pages && row[n] >= 0) ++n;
+  for (; ok < n; ++ok) {
+    if (row[ok] >= p->num_pages || p->refcount[row[ok]] <= 0) break;
+    --p->refcount[row[ok]];
+  }
+  for (int i = 0; i < ok; ++i) ++p->refcount[row[i]];
+  if (ok == n) return n;
+  *bad = row[ok];
+  return -1;
 }
 
 }  // namespace
@@ -206,6 +224,114 @@ int pfkv_pool_release(pfkv_page_pool* pool, const int32_t* block_table_row, int 
   if (i < n_pages)
     return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_release: page %d (entry %d) is not held", block_table_row[i], i);
   for (int k = 0; k < n_pages; ++k) drop_ref(pool, block_table_row[k]);
+  return PFKV_OK;
+}
+
+int pfkv_pool_fork(pfkv_page_pool* pool, const int32_t* block_table_row, int n_pages) {
+  pfkv::clear_error();
+  if (pool == nullptr || (n_pages > 0 && block_table_row == nullptr))
+    return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_fork: null pointer");
+  if (n_pages < 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_fork: bad sizes");
+  for (int i = 0; i < n_pages; ++i) {
+    const int32_t page = block_table_row[i];
+    if (page < 0 || page >= pool->num_pages || pool->refcount[page] <= 0)
+      return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_fork: page %d (entry %d) is not held", page, i);
+  }
+  for (int i = 0; i < n_pages; ++i) pool->refcount[block_table_row[i]] += 1;
+  return PFKV_OK;
+}
+
+int pfkv_pool_resize(pfkv_page_pool* pool, int32_t* block_table_row, uint32_t* table_tags, int max_pages, int n_tokens) {
+  pfkv::clear_error();
+  if (pool == nullptr || block_table_row == nullptr || table_tags == nullptr)
+    return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_resize: null pointer");
+  if (n_tokens < 0 || max_pages <= 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_resize: bad sizes");
+  int32_t bad = 0;
+  const int have = held_pages(pool, block_table_row, max_pages, &bad);
+  if (have < 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_resize: page %d is not held", bad);
+  const int64_t want = ((int64_t)n_tokens + pool->page_size - 1) / pool->page_size;
+  if (want > max_pages)
+    return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_resize: %lld pages needed, row holds %d", (long long)want, max_pages);
+  if (want - have > (int64_t)pool->free_list.size())
+    return pfkv::fail(PFKV_ERR_NO_PAGES, "pool_resize: %lld free pages needed, %lld left", (long long)want - have,
+                      (long long)pool->free_list.size());
+  for (int i = have; i < want; ++i) {
+    block_table_row[i] = take_page(pool);
+    table_tags[i] = pool->tag[block_table_row[i]];
+  }
+  for (int i = (int)want; i < have; ++i) {
+    drop_ref(pool, block_table_row[i]);
+    block_table_row[i] = -1;
+    table_tags[i] = 0;
+  }
+  return PFKV_OK;
+}
+
+int pfkv_pool_make_writable(pfkv_page_pool* pool, int32_t* block_table_row, uint32_t* table_tags, int max_pages,
+                            int first_token, int32_t* pair, int* n_pairs) {
+  pfkv::clear_error();
+  if (pool == nullptr || block_table_row == nullptr || table_tags == nullptr || pair == nullptr || n_pairs == nullptr)
+    return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_make_writable: null pointer");
+  if (first_token < 0 || max_pages <= 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_make_writable: bad sizes");
+  int32_t bad = 0;
+  const int have = held_pages(pool, block_table_row, max_pages, &bad);
+  if (have < 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_make_writable: page %d is not held", bad);
+  const int first = first_token / pool->page_size;
+  int64_t fresh = 0;
+  for (int i = first; i < have; ++i) fresh += pool->refcount[block_table_row[i]] > 1;
+  if (fresh > (int64_t)pool->free_list.size())
+    return pfkv::fail(PFKV_ERR_NO_PAGES, "pool_make_writable: %lld free pages needed, %lld left", (long long)fresh,
+                      (long long)pool->free_list.size());
+  *n_pairs = 0;
+  for (int i = first; i < have; ++i) {
+    const int32_t old = block_table_row[i];
+    if (pool->refcount[old] == 1) {
+      leave_prefix(pool, old);
+      continue;
+    }
+    const int32_t page = take_page(pool);
+    pool->refcount[old] -= 1;  // others hold it still
+    block_table_row[i] = page;
+    table_tags[i] = pool->tag[page];
+    if (i == first && first_token % pool->page_size != 0) {
+      pair[0] = old;
+      pair[1] = page;
+      *n_pairs = 1;
+    }
+  }
+  return PFKV_OK;
+}
+
+int pfkv_pool_compact(pfkv_page_pool* pool, int64_t max_moves, int32_t* pairs, int32_t* remap, int64_t* n_moves) {
+  pfkv::clear_error();
+  if (pool == nullptr || remap == nullptr || n_moves == nullptr || (max_moves > 0 && pairs == nullptr))
+    return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_compact: null pointer");
+  if (max_moves < 0) return pfkv::fail(PFKV_ERR_INVALID_ARG, "pool_compact: bad sizes");
+  for (int64_t i = 0; i < pool->num_pages; ++i) remap[i] = (int32_t)i;
+  int64_t moves = 0, to = 0, from = pool->num_pages - 1;
+  for (; moves < max_moves; ++moves) {
+    while (to < from && pool->refcount[(size_t)to] > 0) ++to;
+    while (from > to && pool->refcount[(size_t)from] == 0) --from;
+    if (to >= from) break;
+    pool->refcount[(size_t)to] = pool->refcount[(size_t)from];
+    pool->refcount[(size_t)from] = 0;
+    pool->tag[(size_t)to] += 1;  // handed out
+    if (pool->registered[(size_t)from]) {
+      auto it = pool->prefix.find(pool->page_hash[(size_t)from]);
+      if (it != pool->prefix.end() && it->second == (int32_t)from) it->second = (int32_t)to;
+      pool->page_hash[(size_t)to] = pool->page_hash[(size_t)from];
+      pool->registered[(size_t)to] = 1;
+      pool->registered[(size_t)from] = 0;
+    }
+    pairs[2 * moves] = (int32_t)from;
+    pairs[2 * moves + 1] = (int32_t)to;
+    remap[from] = (int32_t)to;
+  }
+  // as many pages are free as before: the list keeps its size, lowest id on top
+  size_t k = 0;
+  for (int64_t i = pool->num_pages - 1; i >= 0; --i)
+    if (pool->refcount[(size_t)i] == 0) pool->free_list[k++] = (int32_t)i;
+  *n_moves = moves;
   return PFKV_OK;
 }
 

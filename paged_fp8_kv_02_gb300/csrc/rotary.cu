@@ -1,0 +1,401 @@
+// rotary.cu -- rotary positions with several axes: bf16 rows turned by their
+// token's positions, alone or on the way into the paged e4m3 cache.
+//
+// Pair i turns by phi = position[axis_i] * f_i.  f_i / (2 pi) is kept as a
+// 64-bit fraction of a turn: position * turns_i mod 2^64 is the angle's exact
+// fraction of a turn for every 32-bit position, two integer multiplications in
+// place of a range reduction in double precision, of which this GPU has little.
+// Its upper 32 bits as a signed number are the angle in [-1/2, 1/2) turns, which
+// sincospif takes.
+#include <cuda_bf16.h>
+#include <math.h>
+
+#include "pfkv_internal.h"
+#include "pfkv_ptx.cuh"
+
+namespace pfkv {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kMaxTokens = 4;  // tokens a CTA takes at most
+constexpr int kBatch = 4;      // pieces of a thread whose loads are in flight together
+
+struct RotaryArgs {
+  const uint16_t* x[3];  // q, k, v
+  int64_t stride[3];     // elements between tokens
+  uint16_t* q_out;
+  int64_t q_out_stride;
+  uint8_t* cache[2];       // [pages][Hkv][P][D]
+  const float* scale[2];   // read: per tensor (scale_step 0) or per head (1)
+  float* tscale[2];        // written: [pages][Hkv][P]
+  const int64_t* slots;
+  const int32_t* positions;  // [axes][T]
+  int64_t num_slots;
+  int T, Hq, Hkv, D, P, rows, scale_step, rows_per_cta, pitch, in_place;
+  pfkv_rotary r;
+};
+
+// A piece of a row: 8 channels and 8 more, either the two halves of 8 pairs or
+// 16 consecutive channels.
+struct Piece {
+  int lo, hi;  // first channel of each part
+  bool turns;
+};
+
+__device__ __forceinline__ Piece piece_of(const pfkv_rotary& r, int j, bool turning_row) {
+  Piece p;
+  const int turning = r.num_pairs >> 3;
+  p.turns = turning_row && j < turning;
+  if (p.turns && !r.neighbours) {
+    p.lo = r.first + 8 * j;
+    p.hi = p.lo + r.num_pairs;
+  } else if (p.turns) {
+    p.lo = r.first + 16 * j;
+    p.hi = p.lo + 8;
+  } else {
+    int e = 16 * j;
+    if (turning_row) {
+      e -= 16 * turning;
+      if (e >= r.first) e += 2 * r.num_pairs;
+    }
+    p.lo = e;
+    p.hi = e + 8;
+  }
+  return p;
+}
+
+__device__ __forceinline__ void unpack8(const uint4& v, float (&f)[8]) {
+  const uint32_t w[4] = {v.x, v.y, v.z, v.w};
+#pragma unroll
+  for (int k = 0; k < 4; ++k) f[2 * k] = bf16_lo(w[k]), f[2 * k + 1] = bf16_hi(w[k]);
+}
+
+__device__ __forceinline__ uint4 pack8(const float (&f)[8]) {
+  return make_uint4(pack_bf16x2(f[0], f[1]), pack_bf16x2(f[2], f[3]), pack_bf16x2(f[4], f[5]), pack_bf16x2(f[6], f[7]));
+}
+
+__device__ __forceinline__ uint2 encode8(const float (&f)[8], float s) {
+  uint32_t w[2];
+#pragma unroll
+  for (int k = 0; k < 2; ++k) {
+    const uint16_t a = f32x2_to_e4m3x2(__fdiv_rn(f[4 * k], s), __fdiv_rn(f[4 * k + 1], s));
+    const uint16_t b = f32x2_to_e4m3x2(__fdiv_rn(f[4 * k + 2], s), __fdiv_rn(f[4 * k + 3], s));
+    w[k] = (uint32_t)a | ((uint32_t)b << 16);
+  }
+  return make_uint2(w[0], w[1]);
+}
+
+// A CTA takes `tokens` consecutive tokens (blockDim / tokens threads each) and
+// rows_per_cta of their rows: query heads, then keys, then values.  Pieces of a
+// row lie `pitch` threads apart at most, so that a row's maximum (kToken) is a
+// few shuffles.  kPitch: that number where it is known beforehand, or 0.
+template <int kPitch, bool kToken>
+__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, const int tokens) {
+  __shared__ float2 cs[kMaxTokens][PFKV_ROTARY_MAX_PAIRS];
+  const int per_token = kThreads / tokens;
+  const int which_token = threadIdx.x / per_token, tid = threadIdx.x - which_token * per_token;
+  const int t = blockIdx.x * tokens + which_token;
+  if (t < a.T) {
+    for (int i = tid; i < a.r.num_pairs; i += per_token) {
+      const int64_t pos = a.positions[(int64_t)a.r.axis[i] * a.T + t];
+      const uint64_t phase = (uint64_t)pos * a.r.turns[i];
+      float s, c;
+      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+      cs[which_token][i] = make_float2(c, s);
+    }
+  }
+  __syncthreads();
+  if (t >= a.T) return;
+  int64_t slot_page = 0;
+  int slot_row = 0;
+  bool there = false;
+  if (a.slots) {
+    const int64_t slot = a.slots[t];
+    there = slot >= 0 && slot < a.num_slots;
+    slot_page = there ? slot / a.P : 0;
+    slot_row = (int)(slot - slot_page * a.P);
+  }
+  const int pitch = kPitch ? kPitch : a.pitch;
+  const int pieces = a.D >> 4;
+  const int row0 = blockIdx.y * a.rows_per_cta;
+  const int end = min(a.rows - row0, a.rows_per_cta) * pitch;
+  const int end_warp = (end + 31) & ~31;  // whole warps, for the shuffles
+  for (int f0 = tid; f0 < end_warp; f0 += per_token * kBatch) {
+    uint4 lo[kBatch], hi[kBatch];
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int f = f0 + k * per_token;
+      const int row = row0 + f / pitch, j = f % pitch;
+      lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
+      if (f < end && j < pieces) {
+        const int which = row < a.Hq ? 0 : row < a.Hq + a.Hkv ? 1 : 2;
+        const int h = row - (which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv);
+        const Piece p = piece_of(a.r, j, which < 2);
+        if (which > 0 ? there : (p.turns || !a.in_place)) {
+          const uint16_t* const src = a.x[which] + t * a.stride[which] + (int64_t)h * a.D;
+          lo[k] = *reinterpret_cast<const uint4*>(src + p.lo);
+          hi[k] = *reinterpret_cast<const uint4*>(src + p.hi);
+        }
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < kBatch; ++k) {
+      const int f = f0 + k * per_token;
+      if (f >= end_warp) break;
+      const int row = row0 + f / pitch, j = f % pitch;
+      const bool mine = f < end && j < pieces;
+      const int which = row < a.Hq ? 0 : row < a.Hq + a.Hkv ? 1 : 2;
+      const int h = row - (which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv);
+      const Piece p = piece_of(a.r, j, which < 2);
+      float x[8], y[8];
+      unpack8(lo[k], x);
+      unpack8(hi[k], y);
+      if (p.turns && mine) {
+        const float2* const w = cs[which_token] + 8 * j;
+        if (!a.r.neighbours) {
+#pragma unroll
+          for (int i = 0; i < 8; ++i) {
+            const float2 c = w[i];
+            const float u = x[i], v = y[i];
+            x[i] = u * c.x - v * c.y;
+            y[i] = v * c.x + u * c.y;
+          }
+        } else {
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const float2 c = w[i], d = w[i + 4];
+            float u = x[2 * i], v = x[2 * i + 1];
+            x[2 * i] = u * c.x - v * c.y;
+            x[2 * i + 1] = v * c.x + u * c.y;
+            u = y[2 * i], v = y[2 * i + 1];
+            y[2 * i] = u * d.x - v * d.y;
+            y[2 * i + 1] = v * d.x + u * d.y;
+          }
+        }
+      }
+      float m = 0.f;
+      if constexpr (kToken) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
+        for (int o = pitch >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      }
+      if (!mine) continue;
+      if (which == 0) {
+        if (p.turns || !a.in_place) {
+          uint16_t* const dst = a.q_out + t * a.q_out_stride + (int64_t)h * a.D;
+          *reinterpret_cast<uint4*>(dst + p.lo) = pack8(x);
+          *reinterpret_cast<uint4*>(dst + p.hi) = pack8(y);
+        }
+      } else if (there) {
+        const int64_t row_at = (slot_page * a.Hkv + h) * a.P + slot_row;
+        uint8_t* const dst = a.cache[which - 1] + row_at * a.D;
+        uint2 u = make_uint2(0, 0), v = u;
+        float s;
+        if constexpr (kToken) {
+          s = __fdiv_rn(m, 448.f);
+          if (j == 0) a.tscale[which - 1][row_at] = s;
+        } else {
+          s = __ldg(a.scale[which - 1] + (int64_t)h * a.scale_step);
+        }
+        if (!kToken || s != 0.f) u = encode8(x, s), v = encode8(y, s);
+        *reinterpret_cast<uint2*>(dst + p.lo) = u;
+        *reinterpret_cast<uint2*>(dst + p.hi) = v;
+      }
+    }
+  }
+}
+
+int check_rotary(const char* fn, const pfkv_rotary* r, int D) {
+  if (!r) return fail(PFKV_ERR_INVALID_ARG, "%s: null rotary", fn);
+  if (r->num_pairs < 8 || r->num_pairs > PFKV_ROTARY_MAX_PAIRS || r->num_pairs % 8 || r->first < 0 || r->first % 16 ||
+      r->num_axes < 1 || r->num_axes > PFKV_ROTARY_MAX_AXES)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: rotary not filled by rotary_init", fn);
+  for (int i = 0; i < r->num_pairs; ++i)
+    if (r->axis[i] >= r->num_axes) return fail(PFKV_ERR_INVALID_ARG, "%s: rotary not filled by rotary_init", fn);
+  if ((int64_t)r->first + 2 * r->num_pairs > D)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: channels %d..%d turn, head_dim is %d", fn, r->first,
+                r->first + 2 * r->num_pairs - 1, D);
+  return PFKV_OK;
+}
+
+// Token stride of [T][H][D] rows.
+bool good_stride(int64_t stride, int T, int H, int D) {
+  return stride >= (int64_t)H * D && stride % 8 == 0 && stride <= 0x7FFFFFFF;
+}
+
+int check_q(const char* fn, const void* out, int64_t out_stride, const void* x, int64_t x_stride, int T, int H, int D,
+            int* in_place) {
+  if (!out || !x) return fail(PFKV_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (!aligned(out, 16) || !aligned(x, 16)) return fail(PFKV_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if (!good_stride(out_stride, T, H, D) || !good_stride(x_stride, T, H, D))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: token strides are multiples of 8 of at least %lld and below 2^31", fn, (long long)H * D);
+  *in_place = out == x && (out_stride == x_stride || T == 1);
+  if (!*in_place) {
+    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(x);
+    const uint64_t row = (uint64_t)H * D * 2;
+    const uint64_t on = (uint64_t)(T - 1) * out_stride * 2 + row, in = (uint64_t)(T - 1) * x_stride * 2 + row;
+    if (o < i + in && i < o + on) return fail(PFKV_ERR_INVALID_ARG, "%s: output and input overlap", fn);
+  }
+  return PFKV_OK;
+}
+
+int launch(const char* fn, RotaryArgs& a, bool token, cudaStream_t stream) {
+  const int pieces = a.D / 16;
+  a.pitch = pieces;
+  if (token)
+    for (a.pitch = 1; a.pitch < pieces;) a.pitch *= 2;
+  const int sms = device_sm_count();
+  if (sms <= 0) return fail(PFKV_ERR_CUDA, "%s: no device", fn);
+  int tokens = kMaxTokens;
+  while (tokens > 1 && a.T < 2 * sms * tokens) tokens /= 2;
+  int parts = 1;
+  if (tokens == 1)
+    while (parts * 2 * kThreads < a.rows * a.pitch && (int64_t)a.T * parts < sms) parts *= 2;
+  a.rows_per_cta = (a.rows + parts - 1) / parts;
+  parts = (a.rows + a.rows_per_cta - 1) / a.rows_per_cta;
+  const dim3 grid((unsigned)((a.T + (int64_t)tokens - 1) / tokens), (unsigned)parts);
+  if (pieces == 8) {
+    if (token)
+      rotary_kernel<8, true><<<grid, kThreads, 0, stream>>>(a, tokens);
+    else
+      rotary_kernel<8, false><<<grid, kThreads, 0, stream>>>(a, tokens);
+  } else {
+    if (token)
+      rotary_kernel<0, true><<<grid, kThreads, 0, stream>>>(a, tokens);
+    else
+      rotary_kernel<0, false><<<grid, kThreads, 0, stream>>>(a, tokens);
+  }
+  return check_cuda(fn);
+}
+
+}  // namespace
+}  // namespace pfkv
+
+extern "C" {
+
+int pfkv_rotary_init(pfkv_rotary* rotary, const double* frequencies, const int32_t* axes, int num_pairs, int num_axes,
+                     int first, int neighbours) {
+  using namespace pfkv;
+  clear_error();
+  if (!rotary || !frequencies) return fail(PFKV_ERR_INVALID_ARG, "rotary_init: null pointer");
+  if (num_pairs < 8 || num_pairs > PFKV_ROTARY_MAX_PAIRS || num_pairs % 8)
+    return fail(PFKV_ERR_UNSUPPORTED, "rotary_init: %d pairs: a multiple of 8 up to %d", num_pairs, PFKV_ROTARY_MAX_PAIRS);
+  if (num_axes < 1 || num_axes > PFKV_ROTARY_MAX_AXES)
+    return fail(PFKV_ERR_UNSUPPORTED, "rotary_init: %d axes: 1 to %d", num_axes, PFKV_ROTARY_MAX_AXES);
+  if (first < 0 || first % 16) return fail(PFKV_ERR_UNSUPPORTED, "rotary_init: first channel %d: a multiple of 16", first);
+  for (int i = 0; i < num_pairs; ++i) {
+    if (!isfinite(frequencies[i])) return fail(PFKV_ERR_INVALID_ARG, "rotary_init: frequency %d is not finite", i);
+    if (axes && (axes[i] < 0 || axes[i] >= num_axes))
+      return fail(PFKV_ERR_INVALID_ARG, "rotary_init: axis %d of pair %d outside [0, %d)", axes[i], i, num_axes);
+  }
+  *rotary = pfkv_rotary{};
+  rotary->first = first;
+  rotary->num_pairs = num_pairs;
+  rotary->neighbours = neighbours ? 1 : 0;
+  rotary->num_axes = num_axes;
+  for (int i = 0; i < num_pairs; ++i) {
+    // the fraction of a turn, of the magnitude: a negative frequency is its exact opposite
+    const double turn = fabs(frequencies[i]) / 6.283185307179586476925;
+    const double part = ldexp(turn - floor(turn), 64);
+    const uint64_t whole = part >= 18446744073709551616.0 ? 0 : (uint64_t)part;
+    rotary->turns[i] = frequencies[i] < 0 ? 0 - whole : whole;
+    rotary->axis[i] = axes ? (uint8_t)axes[i] : 0;
+  }
+  return PFKV_OK;
+}
+
+int pfkv_rotary_embed(void* out, int64_t out_stride, const void* x, int64_t x_stride, const int32_t* positions,
+                      const pfkv_rotary* rotary, int num_tokens, int num_heads, int head_dim, pfkv_stream_t stream) {
+  using namespace pfkv;
+  clear_error();
+  const char* fn = "rotary_embed";
+  if (num_tokens < 0 || num_heads <= 0 || head_dim <= 0) return fail(PFKV_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (head_dim % 16 || head_dim > 4096)
+    return fail(PFKV_ERR_UNSUPPORTED, "%s: head_dim %d: a multiple of 16 up to 4096", fn, head_dim);
+  if ((int64_t)num_heads * head_dim >= (int64_t)1 << 30) return fail(PFKV_ERR_UNSUPPORTED, "%s: rows too wide", fn);
+  if (int rc = check_rotary(fn, rotary, head_dim)) return rc;
+  if (num_tokens == 0) return PFKV_OK;
+  RotaryArgs a = {};
+  if (int rc = check_q(fn, out, out_stride, x, x_stride, num_tokens, num_heads, head_dim, &a.in_place)) return rc;
+  if (!positions || !aligned(positions, 4)) return fail(PFKV_ERR_INVALID_ARG, "%s: null or misaligned positions", fn);
+  a.x[0] = static_cast<const uint16_t*>(x);
+  a.stride[0] = x_stride;
+  a.q_out = static_cast<uint16_t*>(out);
+  a.q_out_stride = out_stride;
+  a.positions = positions;
+  a.T = num_tokens;
+  a.Hq = a.rows = num_heads;
+  a.D = head_dim;
+  a.P = 1;
+  a.r = *rotary;
+  return launch(fn, a, false, reinterpret_cast<cudaStream_t>(stream));
+}
+
+int pfkv_rotary_append_fp8(void* q_out, int64_t q_out_stride, const void* q, int64_t q_stride, const void* k_new,
+                           int64_t k_stride, const void* v_new, int64_t v_stride, void* k_cache, void* v_cache,
+                           const int64_t* slot_mapping, const int32_t* positions, const pfkv_rotary* rotary,
+                           int num_tokens, int num_q_heads, int num_kv_heads, int head_dim, int page_size,
+                           int64_t num_pages, pfkv_scale_granularity granularity, float* k_scales, float* v_scales,
+                           pfkv_stream_t stream) {
+  using namespace pfkv;
+  clear_error();
+  const char* fn = "rotary_append_fp8";
+  const bool has_q = q_out || q, has_v = v_new || v_cache || v_scales;
+  if (num_tokens < 0 || (has_q && num_q_heads <= 0) || num_kv_heads <= 0 || head_dim <= 0 || page_size <= 0 ||
+      num_pages <= 0)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (head_dim % 16 || head_dim > 4096)
+    return fail(PFKV_ERR_UNSUPPORTED, "%s: head_dim %d: a multiple of 16 up to 4096", fn, head_dim);
+  if (((int64_t)(has_q ? num_q_heads : 0) + 2 * (int64_t)num_kv_heads) * head_dim >= (int64_t)1 << 30)
+    return fail(PFKV_ERR_UNSUPPORTED, "%s: rows too wide", fn);
+  if (granularity == PFKV_SCALE_BLOCK)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: scales per block are written by kv_append_fp8_block after rotary_embed", fn);
+  if (granularity != PFKV_SCALE_TENSOR && granularity != PFKV_SCALE_HEAD && granularity != PFKV_SCALE_TOKEN)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: unknown granularity %d", fn, (int)granularity);
+  const bool token = granularity == PFKV_SCALE_TOKEN;
+  if (token && head_dim > 512) return fail(PFKV_ERR_UNSUPPORTED, "%s: per-token scales need head_dim <= 512", fn);
+  if (int rc = check_rotary(fn, rotary, head_dim)) return rc;
+  if (num_pages > INT64_MAX / page_size / num_kv_heads / head_dim)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: bad sizes", fn);
+  if (num_tokens == 0) return PFKV_OK;
+  RotaryArgs a = {};
+  if (has_q)
+    if (int rc = check_q(fn, q_out, q_out_stride, q, q_stride, num_tokens, num_q_heads, head_dim, &a.in_place)) return rc;
+  if (!k_new || !k_cache || !k_scales || !slot_mapping || !positions)
+    return fail(PFKV_ERR_INVALID_ARG, "%s: null pointer", fn);
+  if (has_v && (!v_new || !v_cache || !v_scales))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: v_new, v_cache and v_scales must all be set or all NULL", fn);
+  if (!aligned(k_new, 16) || !aligned(k_cache, 16) || !aligned(k_scales, 4) || !aligned(slot_mapping, 8) ||
+      !aligned(positions, 4) || (has_v && (!aligned(v_new, 16) || !aligned(v_cache, 16) || !aligned(v_scales, 4))))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: misaligned pointer", fn);
+  if (!good_stride(k_stride, num_tokens, num_kv_heads, head_dim) ||
+      (has_v && !good_stride(v_stride, num_tokens, num_kv_heads, head_dim)))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: token strides are multiples of 8 of at least %lld and below 2^31", fn,
+                (long long)num_kv_heads * head_dim);
+  a.x[0] = static_cast<const uint16_t*>(q);
+  a.x[1] = static_cast<const uint16_t*>(k_new);
+  a.x[2] = static_cast<const uint16_t*>(v_new);
+  a.stride[0] = q_stride;
+  a.stride[1] = k_stride;
+  a.stride[2] = v_stride;
+  a.q_out = static_cast<uint16_t*>(q_out);
+  a.q_out_stride = q_out_stride;
+  a.cache[0] = static_cast<uint8_t*>(k_cache);
+  a.cache[1] = static_cast<uint8_t*>(v_cache);
+  a.scale[0] = a.tscale[0] = k_scales;
+  a.scale[1] = a.tscale[1] = v_scales;
+  a.scale_step = granularity == PFKV_SCALE_HEAD ? 1 : 0;
+  a.slots = slot_mapping;
+  a.positions = positions;
+  a.num_slots = num_pages * page_size;
+  a.T = num_tokens;
+  a.Hq = has_q ? num_q_heads : 0;
+  a.Hkv = num_kv_heads;
+  a.D = head_dim;
+  a.P = page_size;
+  a.rows = a.Hq + num_kv_heads * (has_v ? 2 : 1);
+  a.r = *rotary;
+  return launch(fn, a, token, reinterpret_cast<cudaStream_t>(stream));
+}
+
+}  // extern "C"
