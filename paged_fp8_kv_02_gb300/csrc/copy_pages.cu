@@ -11,8 +11,8 @@ namespace pfkv {
 namespace {
 
 constexpr int kMaxArrays = 128;  // of a launch: its arguments stay below 4 KB
-constexpr int kUnit = 4096;      // bytes of a page that a warp copies
-constexpr int kThreads = 256;
+constexpr int kUnit = 2048;      // bytes of a page that a warp copies
+constexpr int kThreads = 128;
 
 struct CopyArray {
   char* base;
@@ -32,7 +32,7 @@ struct CopyArgs {
 
 template <class T>
 __device__ __forceinline__ void copy_part(char* dst, const char* src, int bytes, int lane) {
-  constexpr int kStep = 8;
+  constexpr int kStep = 4;
   const int n = bytes / (int)sizeof(T);
   T* const d = reinterpret_cast<T*>(dst);
   const T* const s = reinterpret_cast<const T*>(src);
@@ -43,11 +43,11 @@ __device__ __forceinline__ void copy_part(char* dst, const char* src, int bytes,
       if (i0 + 32 * k < n) v[k] = __ldcs(s + i0 + 32 * k);
 #pragma unroll
     for (int k = 0; k < kStep; ++k)
-      if (i0 + 32 * k < n) d[i0 + 32 * k] = v[k];
+      if (i0 + 32 * k < n) __stcs(d + i0 + 32 * k, v[k]);
   }
 }
 
-__global__ void __launch_bounds__(kThreads) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
+__global__ void __launch_bounds__(kThreads, 8) copy_pages_kernel(const __grid_constant__ CopyArgs a) {
   const int lane = threadIdx.x & 31;
   const int64_t step = (int64_t)gridDim.x * (kThreads / 32);
   for (int64_t w = (int64_t)blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); w < a.total; w += step) {
