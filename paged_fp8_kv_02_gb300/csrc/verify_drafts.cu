@@ -18,10 +18,11 @@
 namespace pfkv {
 namespace {
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 constexpr int kMaxCluster = 8;
-constexpr int kUnroll = 8;  // loads of a lane in flight, of each of the two rows
+constexpr int kVectors = 4;  // 16-byte loads of a lane in flight, of each of the two rows
+constexpr int kWords = 8;    // single words, where the rows cannot be read in 16 bytes alike
 
 struct VerifyArgs {
   int32_t* next;
@@ -34,7 +35,7 @@ struct VerifyArgs {
   const int32_t* q_start;
   int32_t* context_lens;
   int32_t* status;
-  int T, V, stretch;  // stretch: words of the vocabulary per warp
+  int T, V;
 };
 
 __device__ __forceinline__ float to_float(float x) { return x; }
@@ -42,9 +43,7 @@ __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162f
 __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
 
 // floor(2^42 min(max(x, 0), 1)); 0 for NaN.
-__device__ __forceinline__ uint64_t whole(float x) {
-  return (uint64_t)(fminf(fmaxf(x, 0.f), 1.f) * 4398046511104.f);
-}
+__device__ __forceinline__ uint64_t whole(float x) { return (uint64_t)(__saturatef(x) * 4398046511104.f); }
 
 __device__ __forceinline__ uint64_t warp_sum(uint64_t x) {
 #pragma unroll
@@ -61,113 +60,187 @@ __device__ __forceinline__ void store_in_cta(uint64_t* p, int rank, uint64_t v) 
   asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(at), "l"(v) : "memory");
 }
 
-// How a row's weights are made: the target's probabilities less the draft's, or
-// less one at a drafted token, or as they are.
-enum Kind { kMinusDraft, kMinusToken, kPlain };
-
+// The probabilities of one row of a request and what is taken off them: the
+// draft's row (q), or one at a drafted token (token >= 0), or nothing.
 template <class T>
 struct Row {
   const T* p;
   const T* q;
-  int token;
-  Kind kind;
+  int token, V;
   __device__ __forceinline__ uint64_t at(int i) const {
     float x = to_float(p[i]);
-    if (kind == kMinusDraft) x -= to_float(q[i]);
-    if (kind == kMinusToken && i == token) x -= 1.f;
+    if (q) x -= to_float(q[i]);
+    if (i == token) x -= 1.f;
     return whole(x);
   }
 };
 
+// The words of one load, as fp32.
+template <class T, int kSize>
+struct Load;
 template <class T>
-__device__ __forceinline__ uint64_t sum_stretch(const Row<T>& row, int begin, int end, int lane) {
+struct Load<T, 1> {
+  T x;
+  __device__ __forceinline__ void from(const T* p) { x = *p; }
+  __device__ __forceinline__ void zero() { x = T(0.f); }
+  __device__ __forceinline__ float at(int) const { return to_float(x); }
+};
+template <>
+struct Load<float, 4> {
+  float4 x;
+  __device__ __forceinline__ void from(const float* p) { x = __ldcs(reinterpret_cast<const float4*>(p)); }
+  __device__ __forceinline__ void zero() { x = make_float4(0.f, 0.f, 0.f, 0.f); }
+  __device__ __forceinline__ float at(int e) const { return e == 0 ? x.x : e == 1 ? x.y : e == 2 ? x.z : x.w; }
+};
+struct Load16 {
+  uint4 x;
+  __device__ __forceinline__ void zero() { x = make_uint4(0, 0, 0, 0); }
+  __device__ __forceinline__ uint32_t pair(int e) const { return e < 2 ? x.x : e < 4 ? x.y : e < 6 ? x.z : x.w; }
+};
+template <>
+struct Load<__nv_bfloat16, 8> : Load16 {
+  __device__ __forceinline__ void from(const __nv_bfloat16* p) { x = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ float at(int e) const { return e & 1 ? bf16_hi(pair(e)) : bf16_lo(pair(e)); }
+};
+template <>
+struct Load<__half, 8> : Load16 {
+  __device__ __forceinline__ void from(const __half* p) { x = __ldcs(reinterpret_cast<const uint4*>(p)); }
+  __device__ __forceinline__ float at(int e) const { return e & 1 ? f16_hi(pair(e)) : f16_lo(pair(e)); }
+};
+
+// The sum of a warp's part of the row's weights.  Places count from `shift` words
+// before the row, where the 16 bytes begin that hold its first word; a part begins
+// and ends at a multiple of kSize places.  Words of 16 bytes that reach beyond the
+// row are read one by one.
+// A weight is split in two halves of 21 bits without a conversion (one to 64-bit
+// integers takes longer than the loads): x + 4 rounded towards zero holds floor(2^21
+// x) in its lowest bits, and the rest, which is exact, plus 2^-19 likewise the next
+// 21; the bits are summed as integers and the constants' taken off.
+template <class T, int kSize, bool kMinus>
+__device__ __forceinline__ uint64_t sum_part(const Row<T>& row, int shift, int begin, int end, int lane) {
+  constexpr int kDeep = kSize == 1 ? kWords : kVectors;
   uint64_t sum = 0;
-  for (int i0 = begin + lane; i0 < end; i0 += 32 * kUnroll) {
-    float p[kUnroll], q[kUnroll];
+  const int stop = min(end - shift, row.V - kSize + 1);
+  for (int i0 = begin - shift + lane * kSize; i0 < stop; i0 += 32 * kSize * kDeep) {
+    Load<T, kSize> p[kDeep], q[kDeep];
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      const int i = i0 + 32 * k;
-      p[k] = q[k] = 0.f;
-      if (i < end) {
-        p[k] = to_float(row.p[i]);
-        if (row.kind == kMinusDraft) q[k] = to_float(row.q[i]);
+    for (int k = 0; k < kDeep; ++k) {
+      const int i = i0 + 32 * kSize * k;
+      if (i >= 0 && i < stop) {
+        p[k].from(row.p + i);
+        if (kMinus) q[k].from(row.q + i);
+      } else {
+        p[k].zero();
+        if (kMinus) q[k].zero();
       }
     }
+    uint32_t high = 0, low = 0;
 #pragma unroll
-    for (int k = 0; k < kUnroll; ++k) {
-      if (row.kind == kMinusToken && i0 + 32 * k == row.token) q[k] = 1.f;
-      sum += whole(p[k] - q[k]);
-    }
+    for (int k = 0; k < kDeep; ++k)
+#pragma unroll
+      for (int e = 0; e < kSize; ++e) {
+        const float x = __saturatef(kMinus ? p[k].at(e) - q[k].at(e) : p[k].at(e));
+        const float u = __fadd_rz(x, 4.f);
+        const float v = __fadd_rz(x - (u - 4.f), 1.9073486328125e-6f);  // 2^-19
+        high += __float_as_uint(u);
+        low += __float_as_uint(v);
+      }
+    constexpr uint32_t n = kDeep * kSize;  // at most 64: the sums stay below 2^27
+    sum += ((uint64_t)(high - n * 0x40800000u) << 21) + (low - n * 0x36000000u);
   }
+  if (kSize > 1) {
+    // the row's first words, before a multiple of 16 bytes, and its last
+    const int head = shift ? min(kSize - shift, row.V) : 0;
+    const int tail = max(head, (shift + row.V) / kSize * kSize - shift);
+    if (begin == 0 && lane < head) sum += row.at(lane);
+    if (tail + shift >= begin && tail + shift < end && tail + lane < row.V) sum += row.at(tail + lane);
+  }
+  return sum;
+}
+
+template <class T>
+__device__ __forceinline__ uint64_t sum_row(const Row<T>& row, bool wide, int shift, int begin, int end, int lane) {
+  constexpr int kSize = 16 / sizeof(T);
+  Row<T> all = row;  // with the drafted token's word counted as it is
+  all.token = -1;
+  uint64_t sum;
+  if (row.q)
+    sum = wide ? sum_part<T, kSize, true>(all, shift, begin, end, lane) : sum_part<T, 1, true>(all, shift, begin, end, lane);
+  else
+    sum = sum_part<T, kSize, false>(all, shift, begin, end, lane);
+  const int at = row.token + shift;
+  if (row.token >= 0 && lane == 0 && at >= begin && at < end) sum += row.at(row.token) - all.at(row.token);
   return warp_sum(sum);
 }
 
 template <class T>
-__global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyArgs a) {
+__global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_drafts_kernel(const VerifyArgs a) {
   __shared__ uint64_t totals[2][kMaxCluster];  // of each CTA, by pass
   __shared__ uint64_t sums[kWarps];
   __shared__ uint64_t scan[kWarps];
-  __shared__ int found_s[2];
+  __shared__ int found[3];  // drafts that stay, whether a token outside ended them, the token behind them
   const int nc = (int)tc::cluster_nctarank(), rank = (int)tc::cluster_ctarank();
   const int b = blockIdx.x / nc;
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int s0 = a.q_start[b], s1 = a.q_start[b + 1];
   const int n = s1 - s0;
-  if (s0 < 0 || s1 < s0 || s1 > a.T || n == 0) {  // the whole cluster leaves
+  if (s0 < 0 || s1 <= s0 || s1 > a.T) {  // the whole cluster leaves
     if (rank == 0 && threadIdx.x == 0) {
       a.accepted[b] = 0;
-      if (a.status) a.status[b] = n == 0 && s0 >= 0 && s1 <= a.T ? 0 : PFKV_REQ_BAD_INDEX;
+      if (a.status) a.status[b] = s1 == s0 && s0 >= 0 && s1 <= a.T ? 0 : PFKV_REQ_BAD_INDEX;
     }
     return;
   }
   cluster_arrive();  // this CTA is running: its shared memory may be written
+  const float u = a.uniforms[s1 - 1];
   const T* const target = static_cast<const T*>(a.target);
   const T* const draft = static_cast<const T*>(a.draft);
   if (warp == 0) {
-    int kept = n - 1, bad = 0;
+    int kept = n - 1, bad = 0, token = -1;
     for (int j0 = 0; j0 < n - 1; j0 += 32) {
-      const int i = s0 + j0 + lane;
-      bool rejects = false, outside = false;
+      const int64_t i = s0 + j0 + lane;
+      bool rejects = false;
+      int x = 0;
       if (j0 + lane < n - 1) {
-        const int x = a.tokens[i + 1];
-        const float u = a.uniforms[i];
-        outside = x < 0 || x >= a.V;
+        x = a.tokens[i + 1];
+        const float chance = a.uniforms[i];
         rejects = true;
-        if (!outside) {
+        if (x >= 0 && x < a.V) {
           const double p = to_float(target[i * a.target_stride + x]);
           const double q = draft ? to_float(draft[i * a.draft_stride + x]) : 1.f;
-          rejects = !((double)u * q < p);
+          rejects = !((double)chance * q < p);
         }
       }
       const unsigned r = __ballot_sync(0xFFFFFFFFu, rejects);
       if (r) {
         const int first = __ffs(r) - 1;
         kept = j0 + first;
-        bad = __shfl_sync(0xFFFFFFFFu, outside ? 1 : 0, first);
+        token = __shfl_sync(0xFFFFFFFFu, x, first);
+        bad = token < 0 || token >= a.V;
         break;
       }
     }
-    if (lane == 0) found_s[0] = kept, found_s[1] = bad;
+    if (lane == 0) found[0] = kept, found[1] = bad, found[2] = bad ? -1 : token;
   }
   __syncthreads();
-  const int kept = found_s[0], bad_token = found_s[1];
+  const int kept = found[0];
+  const bool rejected = kept < n - 1;
   const int64_t r = s0 + kept;
   Row<T> row;
+  row.V = a.V;
   row.p = target + r * a.target_stride;
-  row.q = draft ? draft + r * a.draft_stride : nullptr;
-  row.token = -1;
-  row.kind = kPlain;
-  if (kept < n - 1) {
-    row.kind = draft ? kMinusDraft : kMinusToken;
-    row.token = a.tokens[r + 1];
-  }
-  const float u = a.uniforms[s1 - 1];
-  const uint32_t U = (uint32_t)(fminf(fmaxf(u, 0.f), 0.99999994f) * 16777216.f);
-  const int first = (rank * kWarps + warp) * a.stretch;
-  const int begin = min(first, a.V), end = min(first + a.stretch, a.V);
+  row.q = draft && rejected ? draft + r * a.draft_stride : nullptr;
+  row.token = draft ? -1 : found[2];
+  // where the two rows stand alike within 16 bytes they are read 16 bytes at a time
+  const int p_at = (int)(reinterpret_cast<uintptr_t>(row.p) & 15), q_at = (int)(reinterpret_cast<uintptr_t>(row.q) & 15);
+  const bool wide = !row.q || p_at == q_at;
+  const int shift = wide ? p_at / (int)sizeof(T) : 0;
+  const int places = shift + a.V, unit = 512 / (int)sizeof(T);  // a unit: one wide load of a warp
+  const int part = (places + nc * kWarps * unit - 1) / (nc * kWarps * unit) * unit;
+  const int begin = min((rank * kWarps + warp) * part, places), end = min(begin + part, places);
   uint64_t total = 0, before = 0;
   for (int pass = 0;; ++pass) {
-    const uint64_t mine = sum_stretch(row, begin, end, lane);
+    const uint64_t mine = sum_row(row, wide, shift, begin, end, lane);
     if (lane == 0) sums[warp] = mine;
     __syncthreads();
     uint64_t all = 0;
@@ -182,7 +255,8 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyArg
       total += totals[pass][k];
     }
     if (total != 0 || pass == 1) break;
-    row.kind = kPlain;
+    row.q = nullptr;  // nothing is left: the target's own weights
+    row.token = -1;
   }
   if (rank == 0) {
     for (int i = threadIdx.x; i < n; i += kThreads)
@@ -190,12 +264,13 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyArg
     if (threadIdx.x == 0) {
       a.accepted[b] = kept;
       if (total == 0) a.next[r] = -1;
-      if (a.status) a.status[b] = (bad_token ? PFKV_REQ_BAD_TOKEN : 0) | (total == 0 ? PFKV_REQ_NO_MASS : 0);
+      if (a.status) a.status[b] = (found[1] ? PFKV_REQ_BAD_TOKEN : 0) | (total == 0 ? PFKV_REQ_NO_MASS : 0);
       if (a.context_lens) a.context_lens[b] -= n - 1 - kept;
     }
   }
   if (total == 0) return;
   // floor(total * U / 2^24), total < 2^62
+  const uint32_t U = (uint32_t)(fminf(fmaxf(u, 0.f), 0.99999994f) * 16777216.f);
   const uint64_t bar = (__umul64hi(total, U) << 40) | ((total * U) >> 24);
   uint64_t own = 0;
   for (int k = 0; k < kWarps; ++k) own += sums[k];
@@ -203,13 +278,15 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyArg
   uint64_t rest = bar - before;
   int holder = 0;
   while (rest >= sums[holder]) rest -= sums[holder++];
-  // this CTA reads the holder's stretch again, a run of words per thread
-  const int h0 = min((rank * kWarps + holder) * a.stretch, a.V), h1 = min(h0 + a.stretch, a.V);
+  // this CTA reads the holder's part again, a run of words per thread
+  const int h0 = max((rank * kWarps + holder) * part - shift, 0);
+  const int h1 = min((rank * kWarps + holder + 1) * part - shift, a.V);
   const int run = (h1 - h0 + kThreads - 1) / kThreads;
   const int i0 = min(h0 + (int)threadIdx.x * run, h1), i1 = min(i0 + run, h1);
-  uint64_t part = 0;
-  for (int i = i0; i < i1; ++i) part += row.at(i);
-  uint64_t upto = part;  // inclusive prefix over the CTA
+  uint64_t mine = 0;
+#pragma unroll 4
+  for (int i = i0; i < i1; ++i) mine += row.at(i);
+  uint64_t upto = mine;  // inclusive prefix over the CTA
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
     const uint64_t y = __shfl_up_sync(0xFFFFFFFFu, upto, o);
@@ -218,8 +295,8 @@ __global__ void __launch_bounds__(kThreads) verify_drafts_kernel(const VerifyArg
   if (lane == 31) scan[warp] = upto;
   __syncthreads();
   for (int k = 0; k < warp; ++k) upto += scan[k];
-  if (rest < upto && rest >= upto - part) {
-    uint64_t left = rest - (upto - part);
+  if (rest < upto && rest >= upto - mine) {
+    uint64_t left = rest - (upto - mine);
     for (int i = i0; i < i1; ++i) {
       const uint64_t w = row.at(i);
       if (left < w) {
@@ -276,9 +353,10 @@ extern "C" int pfkv_verify_drafts(int32_t* next_tokens, int32_t* accepted, const
     return fail(PFKV_ERR_INVALID_ARG, "verify_drafts: rows are at least vocab_size elements apart");
   const int sms = device_sm_count();
   if (sms <= 0) return fail(PFKV_ERR_CUDA, "verify_drafts: no device");
-  int cluster = kMaxCluster;
-  while (cluster > 1 && (int64_t)batch * cluster > 2 * sms) cluster /= 2;
-  while (cluster > 1 && vocab_size < 4096 * cluster) cluster /= 2;
+  int cluster = (int)(4 * sms / (int64_t)batch);  // four CTAs per SM are resident
+  if (cluster > kMaxCluster) cluster = kMaxCluster;
+  if (cluster > (vocab_size + 4095) / 4096) cluster = (vocab_size + 4095) / 4096;
+  if (cluster < 1) cluster = 1;
   VerifyArgs a;
   a.next = next_tokens;
   a.accepted = accepted;
@@ -293,7 +371,6 @@ extern "C" int pfkv_verify_drafts(int32_t* next_tokens, int32_t* accepted, const
   a.status = request_status;
   a.T = num_tokens;
   a.V = vocab_size;
-  a.stretch = ((vocab_size + cluster * kWarps - 1) / (cluster * kWarps) + 31) / 32 * 32;
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   switch (prob_dtype) {
     case PFKV_PROB_F32: return launch<float>(a, batch, cluster, s);
