@@ -18,7 +18,8 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens a CTA takes at most
-constexpr int kBatch = 4;      // pieces of a thread whose loads are in flight together
+constexpr int kBatch = 2;      // query rows of a thread that are in flight together
+constexpr int kBlocks = 4;     // CTAs of an SM, for the registers
 
 struct RotaryArgs {
   const uint16_t* x[3];  // q, k, v
@@ -42,24 +43,20 @@ struct Piece {
   bool turns;
 };
 
-__device__ __forceinline__ Piece piece_of(const pfkv_rotary& r, int j, bool turning_row) {
+__device__ __forceinline__ Piece piece_of(const pfkv_rotary& r, int j) {
   Piece p;
   const int turning = r.num_pairs >> 3;
-  p.turns = turning_row && j < turning;
+  p.turns = j < turning;
   if (p.turns && !r.neighbours) {
     p.lo = r.first + 8 * j;
     p.hi = p.lo + r.num_pairs;
   } else if (p.turns) {
     p.lo = r.first + 16 * j;
     p.hi = p.lo + 8;
-  } else {
-    int e = 16 * j;
-    if (turning_row) {
-      e -= 16 * turning;
-      if (e >= r.first) e += 2 * r.num_pairs;
-    }
-    p.lo = e;
-    p.hi = e + 8;
+  } else {  // the channels before the turning ones, then those behind
+    p.lo = 16 * (j - turning);
+    if (p.lo >= r.first) p.lo += 2 * r.num_pairs;
+    p.hi = p.lo + 8;
   }
   return p;
 }
@@ -85,122 +82,154 @@ __device__ __forceinline__ uint2 encode8(const float (&f)[8], float s) {
   return make_uint2(w[0], w[1]);
 }
 
-// A CTA takes `tokens` consecutive tokens (blockDim / tokens threads each) and
-// rows_per_cta of their rows: query heads, then keys, then values.  Pieces of a
-// row lie `pitch` threads apart at most, so that a row's maximum (kToken) is a
-// few shuffles.  kPitch: that number where it is known beforehand, or 0.
+// Turns the 8 pairs of a piece: x, y are its two halves, or 16 neighbours.
+__device__ __forceinline__ void turn(float (&x)[8], float (&y)[8], const float (&c)[8], const float (&s)[8], bool neighbours) {
+  if (!neighbours) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float u = x[i], v = y[i];
+      x[i] = u * c[i] - v * s[i];
+      y[i] = v * c[i] + u * s[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      float u = x[2 * i], v = x[2 * i + 1];
+      x[2 * i] = u * c[i] - v * s[i];
+      x[2 * i + 1] = v * c[i] + u * s[i];
+      u = y[2 * i], v = y[2 * i + 1];
+      y[2 * i] = u * c[i + 4] - v * s[i + 4];
+      y[2 * i + 1] = v * c[i + 4] + u * s[i + 4];
+    }
+  }
+}
+
+// A CTA takes `tokens` consecutive tokens (kThreads / tokens threads each) and
+// rows_per_cta of their rows: query heads, then keys, then values.  A thread has
+// the same piece of every row that it takes, so that its place in the row and its
+// 8 sines and cosines are found once; a row's pieces lie in consecutive threads
+// (for kToken in a power of two of them, so that its maximum is a few shuffles).
+// The first rows are on their way while the angles are worked out.  kPitch:
+// threads of a row where that is known beforehand, or 0.
 template <int kPitch, bool kToken>
-__global__ void __launch_bounds__(kThreads) rotary_kernel(const __grid_constant__ RotaryArgs a, const int tokens) {
-  __shared__ float2 cs[kMaxTokens][PFKV_ROTARY_MAX_PAIRS];
+__global__ void __launch_bounds__(kThreads, kBlocks) rotary_kernel(const __grid_constant__ RotaryArgs a, const int tokens) {
+  __shared__ __align__(16) float cosine[kMaxTokens][PFKV_ROTARY_MAX_PAIRS], sine[kMaxTokens][PFKV_ROTARY_MAX_PAIRS];
   const int per_token = kThreads / tokens;
   const int which_token = threadIdx.x / per_token, tid = threadIdx.x - which_token * per_token;
   const int t = blockIdx.x * tokens + which_token;
+  const int pitch = kPitch ? kPitch : a.pitch;
+  const int step = per_token / pitch;  // rows of a pass
+  const int r0 = tid / pitch, j = tid - r0 * pitch;
+  const bool live = t < a.T && r0 < step && j < (a.D >> 4);
+  const Piece p = piece_of(a.r, j);
+  const int row0 = blockIdx.y * a.rows_per_cta, row1 = min(a.rows, row0 + a.rows_per_cta);
+  const int64_t slot = t < a.T && a.slots ? a.slots[t] : -1;
+  int64_t pos = 0;
+  if (t < a.T && tid < a.r.num_pairs) pos = a.positions[(int64_t)a.r.axis[tid] * a.T + t];
+
+  // queries: the first rows
+  const int q_end = live && (p.turns || !a.in_place) ? min(row1, a.Hq) : 0;
+  const uint16_t* const q = a.x[0] + t * a.stride[0];
+  uint4 lo[kBatch], hi[kBatch];
+  int row = row0 + r0;
+#pragma unroll
+  for (int k = 0; k < kBatch; ++k) {
+    if (row + k * step < q_end) {
+      const uint16_t* const src = q + (row + k * step) * a.D;
+      lo[k] = __ldcs(reinterpret_cast<const uint4*>(src + p.lo));
+      hi[k] = __ldcs(reinterpret_cast<const uint4*>(src + p.hi));
+    }
+  }
   if (t < a.T) {
     for (int i = tid; i < a.r.num_pairs; i += per_token) {
-      const int64_t pos = a.positions[(int64_t)a.r.axis[i] * a.T + t];
+      if (i != tid) pos = a.positions[(int64_t)a.r.axis[i] * a.T + t];
+      // the angle is (near + rest) turns: 24 bits that fp32 holds, and the next 32
       const uint64_t phase = (uint64_t)pos * a.r.turns[i];
+      const uint32_t near = ((uint32_t)(phase >> 32) + 0x80u) & ~0xFFu;
+      const float rest = (float)(int32_t)((phase - ((uint64_t)near << 32)) >> 8) * 8.719671e-17f;  // 2 pi 2^-56
       float s, c;
-      sincospif((float)(int32_t)(phase >> 32) * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-      cs[which_token][i] = make_float2(c, s);
+      sincospif((float)(int32_t)near * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
+      cosine[which_token][i] = fmaf(-rest, s, c);
+      sine[which_token][i] = fmaf(rest, c, s);
     }
   }
   __syncthreads();
   if (t >= a.T) return;
-  int64_t slot_page = 0;
-  int slot_row = 0;
-  bool there = false;
-  if (a.slots) {
-    const int64_t slot = a.slots[t];
-    there = slot >= 0 && slot < a.num_slots;
-    slot_page = there ? slot / a.P : 0;
-    slot_row = (int)(slot - slot_page * a.P);
+  float c[8], s[8];
+  if (p.turns) {
+#pragma unroll
+    for (int i = 0; i < 8; i += 4) {
+      const float4 u = *reinterpret_cast<const float4*>(&cosine[which_token][8 * j + i]);
+      const float4 v = *reinterpret_cast<const float4*>(&sine[which_token][8 * j + i]);
+      c[i] = u.x, c[i + 1] = u.y, c[i + 2] = u.z, c[i + 3] = u.w;
+      s[i] = v.x, s[i + 1] = v.y, s[i + 2] = v.z, s[i + 3] = v.w;
+    }
   }
-  const int pitch = kPitch ? kPitch : a.pitch;
-  const int pieces = a.D >> 4;
-  const int row0 = blockIdx.y * a.rows_per_cta;
-  const int end = min(a.rows - row0, a.rows_per_cta) * pitch;
-  const int end_warp = (end + 31) & ~31;  // whole warps, for the shuffles
-  for (int f0 = tid; f0 < end_warp; f0 += per_token * kBatch) {
-    uint4 lo[kBatch], hi[kBatch];
+  uint16_t* const q_out = a.q_out + t * a.q_out_stride;
+  while (row < q_end) {
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int f = f0 + k * per_token;
-      const int row = row0 + f / pitch, j = f % pitch;
-      lo[k] = hi[k] = make_uint4(0, 0, 0, 0);
-      if (f < end && j < pieces) {
-        const int which = row < a.Hq ? 0 : row < a.Hq + a.Hkv ? 1 : 2;
-        const int h = row - (which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv);
-        const Piece p = piece_of(a.r, j, which < 2);
-        if (which > 0 ? there : (p.turns || !a.in_place)) {
-          const uint16_t* const src = a.x[which] + t * a.stride[which] + (int64_t)h * a.D;
-          lo[k] = *reinterpret_cast<const uint4*>(src + p.lo);
-          hi[k] = *reinterpret_cast<const uint4*>(src + p.hi);
+      if (row + k * step < q_end) {
+        uint16_t* const dst = q_out + (row + k * step) * a.D;
+        if (p.turns) {
+          float x[8], y[8];
+          unpack8(lo[k], x);
+          unpack8(hi[k], y);
+          turn(x, y, c, s, a.r.neighbours);
+          lo[k] = pack8(x);
+          hi[k] = pack8(y);
         }
+        __stcs(reinterpret_cast<uint4*>(dst + p.lo), lo[k]);
+        __stcs(reinterpret_cast<uint4*>(dst + p.hi), hi[k]);
       }
     }
+    row += kBatch * step;
 #pragma unroll
     for (int k = 0; k < kBatch; ++k) {
-      const int f = f0 + k * per_token;
-      if (f >= end_warp) break;
-      const int row = row0 + f / pitch, j = f % pitch;
-      const bool mine = f < end && j < pieces;
-      const int which = row < a.Hq ? 0 : row < a.Hq + a.Hkv ? 1 : 2;
-      const int h = row - (which == 0 ? 0 : which == 1 ? a.Hq : a.Hq + a.Hkv);
-      const Piece p = piece_of(a.r, j, which < 2);
-      float x[8], y[8];
-      unpack8(lo[k], x);
-      unpack8(hi[k], y);
-      if (p.turns && mine) {
-        const float2* const w = cs[which_token] + 8 * j;
-        if (!a.r.neighbours) {
-#pragma unroll
-          for (int i = 0; i < 8; ++i) {
-            const float2 c = w[i];
-            const float u = x[i], v = y[i];
-            x[i] = u * c.x - v * c.y;
-            y[i] = v * c.x + u * c.y;
-          }
-        } else {
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const float2 c = w[i], d = w[i + 4];
-            float u = x[2 * i], v = x[2 * i + 1];
-            x[2 * i] = u * c.x - v * c.y;
-            x[2 * i + 1] = v * c.x + u * c.y;
-            u = y[2 * i], v = y[2 * i + 1];
-            y[2 * i] = u * d.x - v * d.y;
-            y[2 * i + 1] = v * d.x + u * d.y;
-          }
-        }
+      if (row + k * step < q_end) {
+        const uint16_t* const src = q + (row + k * step) * a.D;
+        lo[k] = __ldcs(reinterpret_cast<const uint4*>(src + p.lo));
+        hi[k] = __ldcs(reinterpret_cast<const uint4*>(src + p.hi));
       }
-      float m = 0.f;
-      if constexpr (kToken) {
+    }
+  }
+  if (slot < 0 || slot >= a.num_slots || row1 <= a.Hq) return;
+
+  // keys, then values
+  const int64_t page = slot <= 0x7FFFFFFF ? (uint32_t)slot / (uint32_t)a.P : slot / a.P;
+  const int64_t slot_at = page * a.Hkv * a.P + (slot - page * a.P);  // of head 0
+  const int kv_end = row1 - a.Hq;
+  const int kv_from = max(row0 - a.Hq, 0);
+  for (int first = kv_from; first < kv_end; first += step) {  // whole warps, for the shuffles
+    const int r = first + r0;
+    const bool mine = live && r < kv_end;
+    const int which = r >= a.Hkv ? 1 : 0, h = r - (which ? a.Hkv : 0);
+    const int lo_at = which ? 16 * j : p.lo, hi_at = which ? 16 * j + 8 : p.hi;
+    float x[8], y[8];
+    if (mine) {
+      const uint16_t* const src = a.x[1 + which] + t * a.stride[1 + which] + h * a.D;
+      unpack8(__ldcs(reinterpret_cast<const uint4*>(src + lo_at)), x);
+      unpack8(__ldcs(reinterpret_cast<const uint4*>(src + hi_at)), y);
+      if (!which && p.turns) turn(x, y, c, s, a.r.neighbours);
+    }
+    float scale, m = 0.f;
+    const int64_t at = slot_at + (int64_t)h * a.P;
+    if constexpr (kToken) {
+      if (mine)
 #pragma unroll
         for (int i = 0; i < 8; ++i) m = fmaxf(m, fmaxf(fabsf(x[i]), fabsf(y[i])));
-        for (int o = pitch >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
-      }
-      if (!mine) continue;
-      if (which == 0) {
-        if (p.turns || !a.in_place) {
-          uint16_t* const dst = a.q_out + t * a.q_out_stride + (int64_t)h * a.D;
-          *reinterpret_cast<uint4*>(dst + p.lo) = pack8(x);
-          *reinterpret_cast<uint4*>(dst + p.hi) = pack8(y);
-        }
-      } else if (there) {
-        const int64_t row_at = (slot_page * a.Hkv + h) * a.P + slot_row;
-        uint8_t* const dst = a.cache[which - 1] + row_at * a.D;
-        uint2 u = make_uint2(0, 0), v = u;
-        float s;
-        if constexpr (kToken) {
-          s = __fdiv_rn(m, 448.f);
-          if (j == 0) a.tscale[which - 1][row_at] = s;
-        } else {
-          s = __ldg(a.scale[which - 1] + (int64_t)h * a.scale_step);
-        }
-        if (!kToken || s != 0.f) u = encode8(x, s), v = encode8(y, s);
-        *reinterpret_cast<uint2*>(dst + p.lo) = u;
-        *reinterpret_cast<uint2*>(dst + p.hi) = v;
-      }
+      for (int o = pitch >> 1; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xFFFFFFFFu, m, o));
+      scale = __fdiv_rn(m, 448.f);
+      if (mine && j == 0) a.tscale[which][at] = scale;
+    } else if (mine) {
+      scale = __ldg(a.scale[which] + (int64_t)h * a.scale_step);
+    }
+    if (mine) {
+      uint2 u = make_uint2(0, 0), v = u;
+      if (!kToken || scale != 0.f) u = encode8(x, scale), v = encode8(y, scale);
+      uint8_t* const dst = a.cache[which] + at * a.D;
+      *reinterpret_cast<uint2*>(dst + lo_at) = u;
+      *reinterpret_cast<uint2*>(dst + hi_at) = v;
     }
   }
 }
@@ -247,7 +276,7 @@ int launch(const char* fn, RotaryArgs& a, bool token, cudaStream_t stream) {
   const int sms = device_sm_count();
   if (sms <= 0) return fail(PFKV_ERR_CUDA, "%s: no device", fn);
   int tokens = kMaxTokens;
-  while (tokens > 1 && a.T < 2 * sms * tokens) tokens /= 2;
+  while (tokens > 1 && (a.T < 2 * sms * tokens || a.pitch * 4 > kThreads / tokens)) tokens /= 2;
   int parts = 1;
   if (tokens == 1)
     while (parts * 2 * kThreads < a.rows * a.pitch && (int64_t)a.T * parts < sms) parts *= 2;
