@@ -210,9 +210,9 @@ PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void
  * A frequency is kept as the fraction of a turn per position in units of 2^-64,
  * so position times frequency wraps exactly in 64-bit integers: a far position
  * costs no more than the frequency's own rounding to double (2^-52 of the angle),
- * and a negative one turns back.  The fraction's upper 32 bits, rounded to fp32,
- * give sine and cosine (angle off by at most 2^-24 rad); pairs turn in fp32 and
- * are rounded once. */
+ * and a negative one turns back (as negative frequencies do: the gradient's turn).
+ * Sine and cosine are fp32, of the fraction's upper 24 bits, corrected to first
+ * order by the next 32; pairs turn in fp32 and are rounded once. */
 #define PFKV_ROTARY_MAX_PAIRS 128
 #define PFKV_ROTARY_MAX_AXES 8
 /* Host description of a model's rotary positions, filled by pfkv_rotary_init
@@ -256,7 +256,7 @@ PFKV_API int pfkv_rotary_embed(void *out, int64_t out_stride, const void *x, int
  *   granularity TENSOR, HEAD: scales are read.  TOKEN: written; the largest
  *               magnitude is taken after the turn (head_dim <= 512).  BLOCK:
  *               an error (rotary_embed, then kv_append_fp8_block).
- * q_out must not overlap k_new or v_new.  Other arguments, layouts, support and
+ * q_out must not overlap k_new or v_new, and a slot is named once.  Other arguments, layouts, support and
  * errors as kv_append_fp8_scaled and rotary_embed. */
 PFKV_API int pfkv_rotary_append_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
                                     const void *k_new, int64_t k_stride, const void *v_new,
@@ -592,7 +592,8 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
  *   draft_probs    likewise; the last row of a request is not read.  NULL: the
  *                  drafts were not sampled (looked up in the prompt, or greedy),
  *                  q_i is 1 at x_i and 0 elsewhere
- *   tokens         int32 [num_tokens]; uniforms fp32 [num_tokens] in [0, 1)
+ *   tokens         int32 [num_tokens] (not next_tokens itself)
+ *   uniforms       fp32 [num_tokens] in [0, 1)
  *   q_start        int32 [batch + 1] (device), as paged_prefill_attn's
  *   context_lens   optional int32 [batch], read and written: L_b (which counted
  *                  all drafts) loses the rejected ones, n_b - 1 - accepted[b]
@@ -602,8 +603,8 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
  *     PFKV_REQ_BAD_TOKEN  a drafted token that was looked at is outside the
  *                         vocabulary: it does not stay
  *     PFKV_REQ_NO_MASS    neither weights have mass: the drawn token is -1
- * A request without rows has accepted 0.  Rows that a broken q_start gives to two
- * requests are written by both.  Probabilities that are NaN or negative
+ * A request without rows has accepted 0; rows behind the last request's stay as
+ * they are.  Rows that a broken q_start gives to two requests are written by both.  Probabilities that are NaN or negative
  * count as 0 in weights, and NaN never accepts.  Nothing waits for the host: the
  * call can be captured, and the rows of K/V behind the new length are
  * overwritten by the next append.

@@ -319,7 +319,7 @@ def _rows(name: str, t, dtype, shape, device: int):
             for n in shape[1:]:
                 row *= n
             return t.data_ptr(), row
-        if shape[0] <= 1 or t[0].is_contiguous():
+        if t[0].is_contiguous() and shape[0] > 1:
             return t.data_ptr(), t.stride(0)
     raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on the call's device {device}, "
                      f"contiguous within a token, got {t.dtype} {tuple(t.shape)}, strides {tuple(t.stride())}, on {t.device}")
@@ -669,7 +669,8 @@ class _PagedArrayStruct(ctypes.Structure):
 class PagedArrays:
     """The tensors that hold a cache's pages, in all layers: K, V, scales,
     bounds, latents, each [pages][...] with what belongs to a page contiguous.
-    Described once, for copy_pages; the tensors are kept."""
+    Described once, for copy_pages; the tensors are kept, and have to keep
+    their memory."""
 
     def __init__(self, tensors):
         self.tensors = list(tensors)

@@ -254,3 +254,34 @@ def test_no_tokens(pf):
     pf.rotary_append_fp8(e, e, e, None, cache, None, torch.empty(0, dtype=torch.int64, device="cuda"), pos, pf.Rotary(FREQ(64)),
                          pf.SCALE_TENSOR, torch.ones(1, device="cuda"))
     assert int((cache != 7).sum()) == 0
+
+
+def test_rows_that_are_not_contiguous_within_a_token_are_refused(pf):
+    import torch
+    rot, pos = pf.Rotary(FREQ(64)), torch.zeros(4, dtype=torch.int32, device="cuda")
+    for T in (1, 4):
+        good = make(T, 4, 128, 1)
+        for bad in (make(T, 128, 4, 1).transpose(1, 2), make(T, 8, 128, 1)[:, ::2], make(T, 4, 256, 1)[..., :128]):
+            assert bad.shape == good.shape
+            for args in ((bad, good), (good, bad)):
+                with pytest.raises(ValueError):
+                    pf.rotary_embed(*args, pos[:T], rot)
+    wide = make(1, 4, 128, 1, 512)   # one token of wider rows
+    out = torch.empty_like(wide)
+    pf.rotary_embed(out, wide, pos[:1], rot)
+    assert torch.equal(out, wide)
+
+
+def test_on_another_device_or_its_stream(pf):
+    """Every tensor of a call on one device, the current one or not."""
+    import torch
+    if torch.cuda.device_count() < 2:
+        pytest.skip("one device")
+    with torch.cuda.device(0):
+        x = make(3, 4, 128, 1).to("cuda:1")
+        out, pos = torch.empty_like(x), torch.arange(3, dtype=torch.int32, device="cuda:1")
+        pf.rotary_embed(out, x, pos, pf.Rotary(FREQ(64)))
+        assert torch.cuda.current_device() == 0
+        want = torch.empty_like(x, device="cuda:0")
+        pf.rotary_embed(want, x.cuda(0), pos.cuda(0), pf.Rotary(FREQ(64)))
+        assert torch.equal(out.cpu(), want.cpu())

@@ -82,6 +82,39 @@ def test_large_vocabularies(pf, V, batch, dtype):
     Case([1 + i % 3 for i in range(batch)], V, dtype, seed=V + batch).check(pf)
 
 
+@pytest.mark.parametrize("dtype,pad,draft", [("float32", 0, True), ("float32", 1, True), ("float16", 3, False)])
+def test_many_requests_of_the_largest_vocabulary(pf, dtype, pad, draft):
+    """A CTA per request and as many blocks per warp as there can be.  The rows
+    are two, over and over, so that the reference is two rows."""
+    import torch
+    B, V = 640, 1 << 20
+    c = Case([1, 2], V, dtype, draft, seed=5)
+    dt, row = c.p.dtype, V + pad
+    p = torch.empty(B * row + 8, dtype=dt, device="cuda")[pad:pad + B * row].view(B, row)[:, :V]
+    p[0::2], p[1::2] = c.p[0], c.p[1]
+    q = None
+    if draft:   # elsewhere in its 16 bytes than the target's rows
+        q = torch.empty(B * (row + pad), dtype=dt, device="cuda").view(B, row + pad)[:, :V]
+        q[0::2], q[1::2] = c.q[0], c.q[1]
+    u = torch.rand(B, device="cuda", generator=torch.Generator(device="cuda").manual_seed(9))
+    u[:6] = torch.tensor([0, 0, 2.0 ** -24, 2.0 ** -24, 1 - 2.0 ** -24, 1 - 2.0 ** -24])
+    i32 = lambda n: torch.empty(n, dtype=torch.int32, device="cuda")
+    for n in (1, 2):   # no drafts; one draft each, outside the vocabulary: always drawn from the first row less the draft's
+        start = torch.arange(0, B + 1, n, dtype=torch.int32, device="cuda")
+        nxt, acc, status = i32(B), i32(B // n), i32(B // n)
+        pf.verify_drafts(nxt, acc, p, q, torch.full_like(nxt, V), u, start, request_status=status)
+        f = lambda t: t.float().cpu().numpy()
+        other = [np.zeros(V, np.float32)] * 2 if n == 1 or not draft else [f(c.q[0])] * 2
+        sums = [np.cumsum(ref.weights(f(c.p[k]), other[k])) for k in (0, 1)]
+        got, chance = nxt.cpu().numpy(), f(u)
+        for b in range(B // n):
+            total = sums[b * n % 2]
+            bar = int(total[-1]) * int(chance[b * n + n - 1] * 2 ** 24) >> 24
+            assert got[b * n] == np.searchsorted(total, bar, side="right"), (n, b)
+        assert (got[1::2] == -1).all() or n == 1
+        assert status.tolist() == [0 if n == 1 else pf.REQ_BAD_TOKEN] * (B // n) and not acc.any()
+
+
 def test_the_accepted_vary(pf):
     """The cases above are no lot of all-or-nothing ones."""
     accepted = Case([8] * 200, 1000, seed=4, near=0.7).check(pf)[1]
@@ -172,6 +205,14 @@ def test_bad_q_start_leaves_rows_alone(pf):
     for change in ([4, 2, 5, 7, 9], [0, 2, 5, 7, 10], [-1, 2, 5, 7, 9], [0, 2, 5, 2 ** 31 - 1, 9], [9, 2, 5, 7, 9]):
         c.q_start = np.array(change, np.int32)
         c.check(pf)
+
+
+def test_rows_behind_the_last_request_stay(pf):
+    """A padded batch: rows and requests that are not there."""
+    c = Case([2, 3, 2, 2], 500, seed=8)
+    c.q_start = np.array([0, 2, 5, 5, 5], np.int32)
+    nxt, acc, _, _ = c.check(pf)
+    assert (nxt[5:] == -7).all() and (acc[2:] == 0).all()
 
 
 def test_graph_replay_and_two_streams(pf):
