@@ -11,6 +11,7 @@ missing or fails to load, importing the binding's functions raises.
 """
 from __future__ import annotations
 
+import array
 import ctypes
 import os
 import threading
@@ -315,10 +316,7 @@ def _rows(name: str, t, dtype, shape, device: int):
     what belongs to one token is contiguous.  ValueError otherwise."""
     if t.dtype is dtype and t.shape == shape and t.get_device() == device:
         if t.is_contiguous():
-            row = 1
-            for n in shape[1:]:
-                row *= n
-            return t.data_ptr(), row
+            return t.data_ptr(), shape[1] * shape[2] if len(shape) == 3 else shape[1]
         if t[0].is_contiguous() and shape[0] > 1:
             return t.data_ptr(), t.stride(0)
     raise ValueError(f"{name}: expected a {dtype} tensor of shape {tuple(shape)} on the call's device {device}, "
@@ -676,18 +674,24 @@ class PagedArrays:
         self.tensors = list(tensors)
         if not self.tensors:
             raise ValueError("no tensors")
-        self.device = self.tensors[0].get_device()
-        self.num_pages = self.tensors[0].shape[0]
-        self._arrays = (_PagedArrayStruct * len(self.tensors))()
+        self.device = device = self.tensors[0].get_device()
+        self.num_pages = pages = self.tensors[0].shape[0] if self.tensors[0].dim() else 0
+        numbers = array.array("q")
         for k, t in enumerate(self.tensors):
-            if not t.is_cuda or t.get_device() != self.device:
-                raise ValueError(f"tensor {k}: on {t.device}, the first one on device {self.device}")
-            if t.dim() < 1 or t.shape[0] != self.num_pages or t.numel() == 0 or not t[0].is_contiguous():
-                raise ValueError(f"tensor {k}: expected [{self.num_pages}][...], contiguous within a page, got "
-                                 f"{tuple(t.shape)} with strides {tuple(t.stride())}")
-            size = t.element_size()
-            page = t[0].numel() * size
-            self._arrays[k] = _PagedArrayStruct(t.data_ptr(), page, t.stride(0) * size if self.num_pages > 1 else page)
+            if device < 0 or t.get_device() != device:
+                raise ValueError(f"tensor {k}: on {t.device}, the first one on device {device}")
+            size = t.nbytes
+            if size and t.dim() and t.shape[0] == pages:
+                page = size // pages
+                if t.is_contiguous():
+                    numbers.extend((t.data_ptr(), page, page))
+                    continue
+                if t[0].is_contiguous():
+                    numbers.extend((t.data_ptr(), page, t.stride(0) * t.element_size() if pages > 1 else page))
+                    continue
+            raise ValueError(f"tensor {k}: expected [{pages}][...], contiguous within a page, got {tuple(t.shape)} with "
+                             f"strides {tuple(t.stride())}")
+        self._arrays = (_PagedArrayStruct * len(self.tensors)).from_buffer(numbers)
         self._ptr = ctypes.addressof(self._arrays)
 
 

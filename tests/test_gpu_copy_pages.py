@@ -151,3 +151,20 @@ def test_replayed_with_other_pairs(pf):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(x, want)
+
+
+def test_arrays_that_are_refused(pf):
+    import torch
+    x = torch.zeros(6, 4, 8, device="cuda")
+    for bad in ([], [x, x[:5]], [x.transpose(1, 2)], [x[:, ::2]], [x[:0]], [x, x.cpu()], [x[0, 0, 0]], [x, torch.zeros(6, 0, device="cuda")],
+                [x[:1].transpose(1, 2)]):
+        with pytest.raises(ValueError):
+            pf.PagedArrays(bad)
+    for good in ([x], [x[:, 1:3]], [x[..., :]], [x[:, 0], x[:, :, 0][:, :1]], [x[::2]]):
+        pf.PagedArrays(good)
+    with pytest.raises(pf.PfkvError):   # pages on top of each other
+        pf.copy_pages(pf.PagedArrays([x[:1].expand(6, 4, 8)]), torch.zeros(1, 2, dtype=torch.int32, device="cuda"))
+    pairs = torch.zeros(1, 2, dtype=torch.int32, device="cuda")
+    for bad in (pairs.long(), pairs[0], pairs.cpu(), torch.zeros(2, 1, dtype=torch.int32, device="cuda")):
+        with pytest.raises(ValueError):
+            pf.copy_pages(pf.PagedArrays([x]), bad)
