@@ -755,13 +755,16 @@ PFKV_API int pfkv_pool_map_request(pfkv_page_pool *pool, const int32_t *tokens, 
  * page, or lists a page more times than it has holders. */
 PFKV_API int pfkv_pool_release(pfkv_page_pool *pool, const int32_t *block_table_row, int n_pages);
 /* Add a holder to each of a request's first n_pages pages: a fork, which
- * shares them all (release each of the two rows once).  PFKV_ERR_INVALID_ARG
- * (nothing changed) if an entry is not a held page. */
+ * shares them all (release each of the two rows once; pfkv_pool_make_writable
+ * before either appends).  PFKV_ERR_INVALID_ARG (nothing changed) if an entry is
+ * not a held page. */
 PFKV_API int pfkv_pool_fork(pfkv_page_pool *pool, const int32_t *block_table_row, int n_pages);
 /* Bring a request to ceil(n_tokens / page_size) pages: fresh pages behind its
  * last one (a context that grows), or its last ones released (rejected drafts,
  * a conversation cut short).  The row's leading entries >= 0 are its pages;
  * entries that change are written (-1 and tag 0 past the last).
+ * A last page that is cut keeps its hash: pfkv_pool_make_writable before other
+ * tokens are appended to it.
  * PFKV_ERR_NO_PAGES or PFKV_ERR_INVALID_ARG (a row of max_pages entries that is
  * too short, an entry that is not held): nothing changed. */
 PFKV_API int pfkv_pool_resize(pfkv_page_pool *pool, int32_t *block_table_row, uint32_t *table_tags,
@@ -814,7 +817,8 @@ PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages
  * the pool calls give no such pairs in one list unless pages are released
  * between the calls that make the list.
  * Any alignment and size; pages and strides that are multiples of 16 bytes are
- * the fast ones.  Supported: page_bytes < 2^31; arrays beyond 128 take another
+ * the fast ones.  No pairs or no arrays: nothing is enqueued.  Supported:
+ * page_bytes < 2^31; arrays beyond 128 take another
  * launch each 128. */
 typedef struct {
   void *base;

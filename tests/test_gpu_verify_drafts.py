@@ -181,6 +181,38 @@ def test_borders_of_the_draw(pf):
             assert c.check(pf)[0].tolist() == [at]
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16"])
+@pytest.mark.parametrize("pads", [(0, 0), (3, 3), (0, 1)])   # rows alike within 16 bytes, shifted alike, and not alike
+@pytest.mark.parametrize("draft", [True, False])
+def test_values_that_are_no_probabilities(pf, dtype, pads, draft):
+    """NaN, infinities and negative numbers anywhere in the rows."""
+    import torch
+    for seed in range(4):
+        c = Case([3] * 40, 5003, dtype, draft, seed=seed)
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        for name, pad in zip("pq", pads):
+            x = getattr(c, name)
+            if x is None:
+                continue
+            y = torch.zeros(c.T, c.V + pad, dtype=x.dtype, device="cuda")[:, :c.V]
+            y.copy_(x)
+            odd = torch.tensor([float("nan"), float("inf"), -float("inf"), -1.0, 2.0, 1e-40, 1.0], device="cuda").to(x.dtype)
+            at = torch.rand(c.T, c.V, device="cuda", generator=g) < (0.001, 0.2, 0.9, 0.0)[seed]
+            which = torch.randint(0, len(odd), (c.T, c.V), device="cuda", generator=g)
+            setattr(c, name, y)
+            y.copy_(torch.where(at, odd[which], x))
+        c.check(pf)
+
+
+def test_the_largest_sums(pf):
+    """Every weight 1: the sums come to 2^62."""
+    c = Case([1, 1, 1], 1 << 20, draft=False)
+    c.p.fill_(1)
+    c.p[1, ::2] = float("inf")
+    c.u = c.u * 0 + c.u.new_tensor([0.0, 0.5, 1 - 2.0 ** -24])
+    assert c.check(pf)[0].tolist() == [0, 1 << 19, (1 << 20) - 1]
+
+
 def test_draws_follow_the_target(pf):
     """What comes out first is distributed as the target, whatever the draft:
     a chi-squared bound of 20,000 requests over 8 words (7 degrees of freedom;
