@@ -28,7 +28,7 @@ constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens a CTA takes at most
 // Query rows of a thread that are in flight together, and CTAs of an SM (64 registers
 // at four).  Prompt of 16,001 and 4,099 tokens, us: 2 rows at 4 CTAs 105.3 and 17.4, 3
-// at 4 104.5 and 18.2, 4 at 3 104.0 and 19.8, 4 at 4 (spilling) 111.0 and 20.2, 2 at 5
+// at 4 104.5 and 18.2, 4 at 3 104.0 and 19.8, 4 at 4 111.0 and 20.2, 2 at 5
 // 111.1 and 20.3.
 constexpr int kBatch = 2;
 constexpr int kBlocks = 4;

@@ -255,15 +255,16 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_drafts_kerne
   row.p = target + r * a.target_stride;
   row.q = draft && rejected ? draft + r * a.draft_stride : nullptr;
   row.token = draft ? -1 : found[2];
-  // where the two rows stand alike within 16 bytes they are read 16 bytes at a time
-  const int p_at = (int)(reinterpret_cast<uintptr_t>(row.p) & 15), q_at = (int)(reinterpret_cast<uintptr_t>(row.q) & 15);
-  const bool wide = !row.q || p_at == q_at;
-  const int shift = wide ? p_at / (int)sizeof(T) : 0;
-  const int places = shift + a.V, block = block_words<T>(wide);
-  const int part = (places + nc * kWarps * block - 1) / (nc * kWarps * block) * block;
-  const int begin = min((rank * kWarps + warp) * part, places), end = min(begin + part, places);
+  int shift, places, block, part;
   uint64_t total = 0, before = 0;
   for (int pass = 0;; ++pass) {
+    // where the two rows stand alike within 16 bytes they are read 16 bytes at a time
+    const int p_at = (int)(reinterpret_cast<uintptr_t>(row.p) & 15), q_at = (int)(reinterpret_cast<uintptr_t>(row.q) & 15);
+    const bool wide = !row.q || p_at == q_at;
+    shift = wide ? p_at / (int)sizeof(T) : 0;
+    places = shift + a.V, block = block_words<T>(wide);
+    part = (places + nc * kWarps * block - 1) / (nc * kWarps * block) * block;
+    const int begin = min((rank * kWarps + warp) * part, places), end = min(begin + part, places);
     constexpr int kSize = 16 / sizeof(T);
     uint64_t mine;
     if (!row.q)

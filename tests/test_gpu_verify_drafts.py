@@ -204,6 +204,28 @@ def test_values_that_are_no_probabilities(pf, dtype, pads, draft):
         c.check(pf)
 
 
+@pytest.mark.parametrize("dtype", ["float32", "bfloat16", "float16"])
+@pytest.mark.parametrize("pads", [(0, 0), (0, 1), (1, 0), (3, 3), (2, 5), (8, 1)])
+@pytest.mark.parametrize("V", [7, 5003, 70001])
+def test_nothing_left_but_the_target(pf, dtype, pads, V):
+    """A draft twice the target everywhere: every draft goes, no weight is
+    left, and the second reading is of the target's row alone, which may stand
+    otherwise within its 16 bytes than both rows together."""
+    import torch
+    c = Case([1 + i % 4 for i in range(30)], V, dtype, seed=V)
+    for name, pad in zip("pq", pads):
+        y = torch.zeros(c.T, V + pad, dtype=c.p.dtype, device="cuda")[:, :V]
+        y.copy_(c.p * (1 if name == "p" else 2))
+        if name == "q":
+            c.q = y
+        else:
+            p = y
+    c.p = p
+    c.u = c.u * 0.4 + 0.55
+    _, accepted, status, _ = c.check(pf)
+    assert not accepted.any() and not status.any()
+
+
 def test_the_largest_sums(pf):
     """Every weight 1: the sums come to 2^62."""
     c = Case([1, 1, 1], 1 << 20, draft=False)
