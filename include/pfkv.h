@@ -211,8 +211,8 @@ PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void
  * so position times frequency wraps exactly in 64-bit integers: a far position
  * costs no more than the frequency's own rounding to double (2^-52 of the angle),
  * and a negative one turns back (as negative frequencies do: the gradient's turn).
- * Sine and cosine are fp32, of the fraction's upper 24 bits, corrected to first
- * order by the next 32; pairs turn in fp32 and are rounded once. */
+ * Sine and cosine are fp32, off by little more than their rounding; pairs turn in
+ * fp32 and are rounded once. */
 #define PFKV_ROTARY_MAX_PAIRS 128
 #define PFKV_ROTARY_MAX_AXES 8
 /* Host description of a model's rotary positions, filled by pfkv_rotary_init

@@ -5,13 +5,12 @@
 // 64-bit fraction of a turn: position * turns_i mod 2^64 is the angle's exact
 // fraction of a turn for every 32-bit position, two integer multiplications in
 // place of a range reduction in double precision, of which this GPU has little.
-// Its upper 24 bits as a signed number in [-1/2, 1/2) are what sincospif takes; the
-// next 32 correct sine and cosine to first order.
+// Sine and cosine of that fraction come from a table and a short polynomial.
 //
 // Prompts are bounded by HBM (16,001 tokens, 64/8 heads of 128, scales per token, 624
 // MB: 105 us on the device, 5.9 TB/s, 88% of a plain copy's rate; 2,039 latent tokens
-// of 128 heads of 576, 605 MB: 100 us; 4,099 tokens of 48 query heads, 101 MB: 17.4
-// us).  A step of 64 tokens takes 3.6 us, queries alone 2.8: the launch and the chain
+// of 128 heads of 576, 605 MB: 100 us; 4,099 tokens of 48 query heads, 101 MB: 17.9
+// us).  A step of 64 tokens takes 3.5 us, queries alone 2.7: the launch and the chain
 // position -> angle -> turn -> store.  What the shape below gained: 168, 130, 23.3
 // and 3.9 us with a piece's place worked out for every row, the angles before the
 // first load and two CTAs per SM.
@@ -27,7 +26,7 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens a CTA takes at most
 // Query rows of a thread that are in flight together, and CTAs of an SM (64 registers
-// at four).  Prompt of 16,001 and 4,099 tokens, us: 2 rows at 4 CTAs 105.3 and 17.4, 3
+// at four).  Prompt of 16,001 and 4,099 tokens, us (with sincospif): 2 rows at 4 CTAs 105.3 and 17.4, 3
 // at 4 104.5 and 18.2, 4 at 3 104.0 and 19.8, 4 at 4 111.0 and 20.2, 2 at 5
 // 111.1 and 20.3.
 constexpr int kBatch = 2;
@@ -47,6 +46,49 @@ struct RotaryArgs {
   int T, Hq, Hkv, D, P, rows, scale_step, rows_per_cta, pitch, in_place;
   pfkv_rotary r;
 };
+
+// cos and sin of i / 128 of a turn, each as the nearest fp32 number and the rest.
+__device__ const float4 kQuarter[32] = {
+    {1.f, 0.f, 0.f, 0.f}, {0.99879545f, 6.47143805e-09f, 0.0490676761f, -1.73993431e-09f},
+    {0.99518472f, 7.10966619e-09f, 0.0980171412f, -8.93393193e-10f}, {0.989176512f, -1.79974535e-09f, 0.146730468f, 6.77824552e-09f},
+    {0.980785251f, 2.97394731e-08f, 0.195090324f, -1.67047143e-09f}, {0.970031261f, -8.24954771e-09f, 0.242980182f, -2.2676041e-09f},
+    {0.956940353f, -1.7184508e-08f, 0.290284663f, 1.38156651e-08f}, {0.941544056f, 9.24430044e-09f, 0.336889863f, -9.62200097e-09f},
+    {0.923879504f, 2.83074897e-08f, 0.382683426f, 6.22335072e-09f}, {0.903989315f, -2.1909516e-08f, 0.427555084f, 9.20176646e-09f},
+    {0.881921291f, -2.70029634e-08f, 0.471396744f, -7.42525375e-09f}, {0.857728601f, 9.49825818e-09f, 0.514102757f, -1.27838593e-08f},
+    {0.831469595f, 1.68702634e-08f, 0.555570245f, -1.17695214e-08f}, {0.803207517f, 1.48104178e-08f, 0.59569931f, -5.81030113e-09f},
+    {0.773010433f, 2.06425526e-08f, 0.634393275f, 9.37955758e-09f}, {0.740951121f, 4.50153514e-09f, 0.671558976f, -2.13263824e-08f},
+    {0.707106769f, 1.21016175e-08f, 0.707106769f, 1.21016175e-08f}, {0.671558976f, -2.13263824e-08f, 0.740951121f, 4.50153514e-09f},
+    {0.634393275f, 9.37955758e-09f, 0.773010433f, 2.06425526e-08f}, {0.59569931f, -5.81030113e-09f, 0.803207517f, 1.48104178e-08f},
+    {0.555570245f, -1.17695214e-08f, 0.831469595f, 1.68702634e-08f}, {0.514102757f, -1.27838593e-08f, 0.857728601f, 9.49825818e-09f},
+    {0.471396744f, -7.42525375e-09f, 0.881921291f, -2.70029634e-08f}, {0.427555084f, 9.20176646e-09f, 0.903989315f, -2.1909516e-08f},
+    {0.382683426f, 6.22335072e-09f, 0.923879504f, 2.83074897e-08f}, {0.336889863f, -9.62200097e-09f, 0.941544056f, 9.24430044e-09f},
+    {0.290284663f, 1.38156651e-08f, 0.956940353f, -1.7184508e-08f}, {0.242980182f, -2.2676041e-09f, 0.970031261f, -8.24954771e-09f},
+    {0.195090324f, -1.67047143e-09f, 0.980785251f, 2.97394731e-08f}, {0.146730468f, 6.77824552e-09f, 0.989176512f, -1.79974535e-09f},
+    {0.0980171412f, -8.93393193e-10f, 0.99518472f, 7.10966619e-09f}, {0.0490676761f, -1.73993431e-09f, 0.99879545f, 6.47143805e-09f},
+};
+
+// Cosine and sine of phase / 2^64 turns, off by little more than their rounding
+// (0.6 of half a step of 1, where sincospif and a correction for the angle's lower
+// bits were off by up to two): the nearest 1/128 of a turn from the table, which the
+// warp's lanes hold (`entry` is this lane's), and a rest of at most 0.0246 rad, for
+// which three terms do (method of P. T. P. Tang, "Table-lookup algorithms for
+// elementary functions and their error analysis", 1991).  By whole warps.
+__device__ __forceinline__ void cos_sin(uint64_t phase, const float4& entry, float* cosine, float* sine) {
+  const uint32_t near = (uint32_t)((phase + (1ull << 56)) >> 57);  // of 128
+  const float r = (float)(int32_t)((int64_t)(phase - ((uint64_t)near << 57)) >> 25) * 1.14290478e-11f;  // 2 pi 2^-39
+  const int lane = near & 31;
+  const float ch = __shfl_sync(0xFFFFFFFFu, entry.x, lane), cl = __shfl_sync(0xFFFFFFFFu, entry.y, lane);
+  const float sh = __shfl_sync(0xFFFFFFFFu, entry.z, lane), sl = __shfl_sync(0xFFFFFFFFu, entry.w, lane);
+  const float r2 = r * r;
+  const float sr = fmaf(r * r2, -0.16666667f, r);            // sin r
+  const float cr = r2 * fmaf(r2, 0.041666668f, -0.5f);       // cos r - 1
+  const float c = ch + fmaf(-sh, sr, fmaf(ch, cr, cl));
+  const float s = sh + fmaf(ch, sr, fmaf(sh, cr, sl));
+  const bool odd = near & 32;  // quarters of a turn
+  const float a = odd ? s : c, b = odd ? c : s;
+  *cosine = ((near + 32) & 64) ? -a : a;
+  *sine = (near & 64) ? -b : b;
+}
 
 // A piece of a row: 8 channels and 8 more, either the two halves of 8 pairs or
 // 16 consecutive channels.
@@ -153,16 +195,16 @@ __global__ void __launch_bounds__(kThreads, kBlocks) rotary_kernel(const __grid_
     }
   }
   if (t < a.T) {
-    for (int i = tid; i < a.r.num_pairs; i += per_token) {
-      if (i != tid) pos = a.positions[(int64_t)a.r.axis[i] * a.T + t];
-      // the angle is (near + rest) turns: 24 bits that fp32 holds, and the next 32
-      const uint64_t phase = (uint64_t)pos * a.r.turns[i];
-      const uint32_t near = ((uint32_t)(phase >> 32) + 0x80u) & ~0xFFu;
-      const float rest = (float)(int32_t)((phase - ((uint64_t)near << 32)) >> 8) * 8.719671e-17f;  // 2 pi 2^-56
-      float s, c;
-      sincospif((float)(int32_t)near * 4.656612873077393e-10f, &s, &c);  // 2^-31: half turns
-      cosine[which_token][i] = fmaf(-rest, s, c);
-      sine[which_token][i] = fmaf(rest, c, s);
+    const float4 entry = __ldg(kQuarter + (threadIdx.x & 31));
+    for (int i = tid; (i & ~31) < a.r.num_pairs; i += per_token) {  // whole warps
+      const bool mine = i < a.r.num_pairs;
+      if (mine && i != tid) pos = a.positions[(int64_t)a.r.axis[i] * a.T + t];
+      float c, s;
+      cos_sin((uint64_t)pos * (mine ? a.r.turns[i] : 0), entry, &c, &s);
+      if (mine) {
+        cosine[which_token][i] = c;
+        sine[which_token][i] = s;
+      }
     }
   }
   __syncthreads();

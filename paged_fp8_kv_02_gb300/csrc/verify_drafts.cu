@@ -10,10 +10,10 @@
 // memory, and the CTA that holds the threshold reads one block again to find the
 // token.
 //
-// 64 requests with up to seven drafts, 128,259 words in fp32 (62 MB): 13.7 us on the
+// 64 requests with up to seven drafts, 128,259 words in fp32 (62 MB): 13.5 us on the
 // device, of which the launch, the chain lengths -> token -> probability in front of
 // the row, the exchange and the block take about 6; 96 with up to five looked-up
-// drafts, 152,064 words in bf16 (29 MB): 11.8; one of 32,768 words: 4.6.  Word by word
+// drafts, 152,064 words in bf16 (29 MB): 11.4; one of 32,768 words: 4.5.  Word by word
 // and with conversions to 64-bit integers these took 25.0, 65.5 and 6.0 us; reading a
 // warp's whole part again for the token 14.1, 13.3 and 4.5.
 #include <cuda_bf16.h>
