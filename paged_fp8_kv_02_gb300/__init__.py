@@ -308,7 +308,12 @@ class Rotary:
         self.num_axes = 1 if num_axes is None else _count("num_axes", num_axes)
         _check("rotary_init", load().pfkv_rotary_init(ctypes.byref(self._struct), fp, ap, f.shape[0], self.num_axes,
                                                       _count("first", first), 1 if neighbours else 0))
-        self._ptr = ctypes.addressof(self._struct)
+
+    @property
+    def _ptr(self) -> int:
+        """Address of the description, taken when it is passed: a copied or
+        unpickled object has a description of its own."""
+        return ctypes.addressof(self._struct)
 
 
 def _rows(name: str, t, dtype, shape, device: int):
