@@ -775,8 +775,9 @@ PFKV_API int pfkv_pool_resize(pfkv_page_pool *pool, int32_t *block_table_row, ui
  * other holders is given up for a fresh one, and pages it holds alone leave the
  * prefix table.  Where the first of them keeps earlier rows (first_token is
  * not a multiple of page_size), pair[0], pair[1] = old, new page and *n_pairs =
- * 1: copy the page (pfkv_copy_pages) before the next holder writes to either;
- * otherwise *n_pairs = 0.  Row and tags are written where pages change.
+ * 1: copy the page (pfkv_copy_pages, which says what pairs may share a call)
+ * before the next holder writes to either; otherwise *n_pairs = 0.  Row and tags
+ * are written where pages change.
  * PFKV_ERR_NO_PAGES, PFKV_ERR_INVALID_ARG: nothing changed. */
 PFKV_API int pfkv_pool_make_writable(pfkv_page_pool *pool, int32_t *block_table_row,
                                      uint32_t *table_tags, int max_pages, int first_token,
@@ -784,9 +785,9 @@ PFKV_API int pfkv_pool_make_writable(pfkv_page_pool *pool, int32_t *block_table_
 /* Move held pages from the highest ids to the lowest free ones, max_moves at
  * most, so that the pool's end can be given back.  pairs[k] = (old, new) page
  * of move k (the pages are distinct: copy them in any order, with one
- * pfkv_copy_pages); remap[num_pages] = the new id of every page.  Holders,
- * prefix entries and fresh tags move along; the caller rewrites its rows
- * (row[i] = remap[row[i]]) and their tags (pfkv_pool_page_tags).  Free pages
+ * pfkv_copy_pages of their own); remap[num_pages] = the new id of every page.
+ * Holders, prefix entries and fresh tags move along; the caller rewrites its
+ * rows (row[i] = remap[row[i]]) and their tags (pfkv_pool_page_tags).  Free pages
  * are handed out lowest id first afterwards. */
 PFKV_API int pfkv_pool_compact(pfkv_page_pool *pool, int64_t max_moves, int32_t *pairs,
                                int32_t *remap, int64_t *n_moves);
@@ -813,9 +814,14 @@ PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages
  *                for a pair that names a page >= num_pages (not copied)
  * A page may be the source of many pairs.  A page that is the destination of
  * two pairs, or the destination of one and the source of another, ends with
- * unspecified bytes of the pages involved (the copies run at the same time);
- * the pool calls give no such pairs in one list unless pages are released
- * between the calls that make the list.
+ * unspecified bytes of the pages involved (the copies run at the same time).
+ * No such pairs are in one list that holds the pairs of one pfkv_pool_compact,
+ * or of pfkv_pool_make_writable calls between which pages were neither shared by
+ * a fork, nor given back (a cut, a release), nor moved by a compact: such a list
+ * is one call.  Pairs from before and from after a fork, a cut, a release or a
+ * compact are calls of their own, in the pool calls' order on one stream (a
+ * compact hands pages that it has emptied out at once; a fork's copy may be the
+ * next fork's source).
  * Any alignment and size; pages and strides that are multiples of 16 bytes are
  * the fast ones.  No pairs or no arrays: nothing is enqueued.  Supported:
  * page_bytes < 2^31; arrays beyond 128 take another

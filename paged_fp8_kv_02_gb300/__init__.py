@@ -704,7 +704,10 @@ def copy_pages(arrays: PagedArrays, pairs, pair_status=None, stream=None):
     """Copy page pairs[i][0] to page pairs[i][1] in every array (pairs int32
     [n][2]; a pair with a negative entry is padding).  No page may be the
     destination of two pairs, or of one and the source of another: its bytes
-    are unspecified then.  pair_status: optional int32 [n]."""
+    are unspecified then.  The pairs of one PagePool.compact, or of
+    make_writable calls without a fork, a cut, a release or a compact between
+    them, may share a call; others take one each, in the order of the pool's
+    calls.  pair_status: optional int32 [n]."""
     import torch
     dev = arrays.device
     n = pairs.shape[0]
@@ -799,7 +802,7 @@ class PagePool:
     def make_writable(self, row, tags, first_token: int):
         """Give a request (row and tags changed in place) pages of its own from
         token first_token on -> int32 [0 or 1][2], the page to copy before it
-        is written (copy_pages)."""
+        is written (copy_pages, which says what pairs may share a call)."""
         import numpy as np
         rp, tp, n = self._row(row, tags)
         pair, k = np.zeros((1, 2), np.int32), ctypes.c_int(0)
@@ -809,7 +812,8 @@ class PagePool:
 
     def compact(self, max_moves: int = None):
         """Move held pages to the lowest free ids -> (int32 [n][2] pages to copy,
-        int32 [num_pages] new id of every page).  The holders' rows follow:
+        with a copy_pages of their own; int32 [num_pages] new id of every page).
+        The holders' rows follow:
         row[row >= 0] = remap[row[row >= 0]], tags from page_tags()."""
         import numpy as np
         most = self.num_pages if max_moves is None else min(max_moves, self.num_pages)
