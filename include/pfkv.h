@@ -231,9 +231,12 @@ PFKV_API int pfkv_rotary_init(pfkv_rotary *rotary, const double *frequencies, co
 /* rotary_embed -- rows of bf16 turned by their token's positions.
  *   out, x      bf16 [num_tokens][num_heads][head_dim]; the elements between two
  *               tokens are the strides (multiples of 8, at least num_heads *
- *               head_dim, below 2^31), so that both may be parts of wider rows.  out == x
- *               with the same stride turns in place (only the turning channels
- *               are written); other overlaps are an error.
+ *               head_dim, below 2^31), so that both may be parts of wider rows.
+ *               out == x with the same stride turns in place (only the turning
+ *               channels are written).  Other overlaps are an error; with one
+ *               stride rows overlap where they have elements in common (parts
+ *               beside each other in the same wider rows have none), with two
+ *               where their extents do
  *   positions   int32 [num_axes][num_tokens]
  * For caches that rotary_append_fp8 does not fill: turned keys go on to
  * kv_append_fp8_block or kv_append_bf16.  Supported: head_dim a multiple of 16

@@ -306,6 +306,20 @@ bool good_stride(int64_t stride, int T, int H, int D) {
   return stride >= (int64_t)H * D && stride % 8 == 0 && stride <= 0x7FFFFFFF;
 }
 
+// Whether rows of `row` and `other_row` bytes, T of each `stride` and `other_stride`
+// bytes apart, have bytes in common.  With one stride (parts of the same wider rows)
+// each row lies at the same place of its wider row: exact.  With two: by extents.
+bool rows_meet(const void* a, int64_t stride, int64_t row, const void* b, int64_t other_stride, int64_t other_row, int T) {
+  uintptr_t lo = reinterpret_cast<uintptr_t>(a), hi = reinterpret_cast<uintptr_t>(b);
+  if (hi < lo) return rows_meet(b, other_stride, other_row, a, stride, row, T);
+  const uint64_t apart = hi - lo;
+  if (apart >= (uint64_t)(T - 1) * stride + row) return false;
+  if (T == 1 || stride != other_stride) return true;
+  // the first row of b begins `in` bytes behind one of a's
+  const uint64_t rows = apart / stride, in = apart % stride;
+  return in < (uint64_t)row || (rows + 1 < (uint64_t)T && in + other_row > (uint64_t)stride);
+}
+
 int check_q(const char* fn, const void* out, int64_t out_stride, const void* x, int64_t x_stride, int T, int H, int D,
             int* in_place) {
   if (!out || !x) return fail(PFKV_ERR_INVALID_ARG, "%s: null pointer", fn);
@@ -313,12 +327,9 @@ int check_q(const char* fn, const void* out, int64_t out_stride, const void* x, 
   if (!good_stride(out_stride, T, H, D) || !good_stride(x_stride, T, H, D))
     return fail(PFKV_ERR_INVALID_ARG, "%s: token strides are multiples of 8 of at least %lld and below 2^31", fn, (long long)H * D);
   *in_place = out == x && (out_stride == x_stride || T == 1);
-  if (!*in_place) {
-    const uintptr_t o = reinterpret_cast<uintptr_t>(out), i = reinterpret_cast<uintptr_t>(x);
-    const uint64_t row = (uint64_t)H * D * 2;
-    const uint64_t on = (uint64_t)(T - 1) * out_stride * 2 + row, in = (uint64_t)(T - 1) * x_stride * 2 + row;
-    if (o < i + in && i < o + on) return fail(PFKV_ERR_INVALID_ARG, "%s: output and input overlap", fn);
-  }
+  const int64_t row = (int64_t)H * D * 2;
+  if (!*in_place && rows_meet(out, out_stride * 2, row, x, x_stride * 2, row, T))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: output and input overlap", fn);
   return PFKV_OK;
 }
 
