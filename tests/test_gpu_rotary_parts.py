@@ -73,3 +73,14 @@ def test_append_of_one_buffer(pf, T, gran):
         all_ = buf.clone()
         part(all_, at[target], Hq).copy_(q_out)
         assert torch.equal(now, all_)
+
+
+@pytest.mark.parametrize("T,H,wide", [(5, 12, 16), (64, 64, 2048), (1300, 4, 8), (3, 7, 0)])
+def test_what_stands_around_the_input_stays(pf, T, H, wide):
+    """Out of place, the input's rows and what lies between them are only read."""
+    import torch
+    buf = rows(T, H * 128 + wide, T)
+    x, before = part(buf, wide // 16 * 8, H), buf.clone()
+    out = torch.empty(T, H, 128, dtype=torch.bfloat16, device="cuda")
+    pf.rotary_embed(out, x, torch.arange(T, dtype=torch.int32, device="cuda") + 1, pf.Rotary(FREQ))
+    assert torch.equal(buf, before) and not torch.equal(out, x)
