@@ -259,8 +259,9 @@ PFKV_API int pfkv_rotary_embed(void *out, int64_t out_stride, const void *x, int
  *   granularity TENSOR, HEAD: scales are read.  TOKEN: written; the largest
  *               magnitude is taken after the turn (head_dim <= 512).  BLOCK:
  *               an error (rotary_embed, then kv_append_fp8_block).
- * q_out must not overlap k_new or v_new, and a slot is named once.  Other arguments, layouts, support and
- * errors as kv_append_fp8_scaled and rotary_embed. */
+ * q_out over k_new or v_new is an error, like q_out over q (in place, or parts of
+ * the same wider rows, are none); a slot is named once.  Other arguments,
+ * layouts, support and errors as kv_append_fp8_scaled and rotary_embed. */
 PFKV_API int pfkv_rotary_append_fp8(void *q_out, int64_t q_out_stride, const void *q, int64_t q_stride,
                                     const void *k_new, int64_t k_stride, const void *v_new,
                                     int64_t v_stride, void *k_cache, void *v_cache,

@@ -470,6 +470,10 @@ int pfkv_rotary_append_fp8(void* q_out, int64_t q_out_stride, const void* q, int
       (has_v && !good_stride(v_stride, num_tokens, num_kv_heads, head_dim)))
     return fail(PFKV_ERR_INVALID_ARG, "%s: token strides are multiples of 8 of at least %lld and below 2^31", fn,
                 (long long)num_kv_heads * head_dim);
+  const int64_t q_row = (int64_t)num_q_heads * head_dim * 2, kv_row = (int64_t)num_kv_heads * head_dim * 2;
+  if (has_q && (rows_meet(q_out, q_out_stride * 2, q_row, k_new, k_stride * 2, kv_row, num_tokens) ||
+                (has_v && rows_meet(q_out, q_out_stride * 2, q_row, v_new, v_stride * 2, kv_row, num_tokens))))
+    return fail(PFKV_ERR_INVALID_ARG, "%s: q_out overlaps k_new or v_new", fn);
   a.x[0] = static_cast<const uint16_t*>(q);
   a.x[1] = static_cast<const uint16_t*>(k_new);
   a.x[2] = static_cast<const uint16_t*>(v_new);

@@ -30,3 +30,28 @@ def test_parts_of_one_buffer():
     # queries of projections that stand in one row with keys and values, turned into a part behind them
     expect(append, NO, q=0x10000, qs=3200, qo=0x10000 + 2 * 1536, qos=3200, k=0x10000 + 2 * 1024, ks=3200, v=0x10000 + 2 * 1280, vs=3200)
     """)
+
+
+def test_queries_over_keys_or_values_are_refused():
+    """q_out is written while k_new and v_new are read."""
+    refuses("""
+    far, row = 0x900000, 3 * 2048
+    for kv, step in (("k", "ks"), ("v", "vs")):
+        expect(append, BAD, **{kv: 0x100000})
+        expect(append, BAD, **{kv: 0x100000 + row - 16})
+        expect(append, BAD, **{kv: 0x100000 - 3 * 512 + 16})
+        expect(append, NO, **{kv: 0x100000 + row})
+        expect(append, NO, **{kv: 0x100000 - 3 * 512})
+        # one row of queries, keys and values: in place, and with the queries' output a head too far
+        wide = dict(q=far, qs=1536, qo=far, qos=1536, k=far + 2048, ks=1536, v=far + 2560, vs=1536)
+        expect(append, NO, **wide)
+        expect(append, BAD, **dict(wide, **{kv: far + 2048 - 256}))
+        expect(append, BAD, **dict(wide, **{kv: far + 3072 - 256}))     # the next token's first head
+        expect(append, NO, **dict(wide, T=1, **{kv: far + 3072 - 256}))
+        expect(append, BAD, **dict(wide, T=1, **{kv: far + 2048 - 256}))
+        expect(append, BAD, **dict(wide, **{step: 1544}))   # another stride: by extents
+        expect(append, NO, **dict(wide, T=1, **{step: 1544}))
+    # no queries, nothing that is written over
+    expect(append, NO, qo=None, q=None, k=0x100000)
+    expect(append, NO, v=None, vc=None, sv=None, vs=0)
+    """)
