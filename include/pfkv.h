@@ -596,7 +596,7 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
  *   draft_probs    likewise; the last row of a request is not read.  NULL: the
  *                  drafts were not sampled (looked up in the prompt, or greedy),
  *                  q_i is 1 at x_i and 0 elsewhere
- *   tokens         int32 [num_tokens] (not next_tokens itself)
+ *   tokens         int32 [num_tokens]
  *   uniforms       fp32 [num_tokens] in [0, 1)
  *   q_start        int32 [batch + 1] (device), as paged_prefill_attn's
  *   context_lens   optional int32 [batch], read and written: L_b (which counted
@@ -608,10 +608,13 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
  *                         vocabulary: it does not stay
  *     PFKV_REQ_NO_MASS    neither weights have mass: the drawn token is -1
  * A request without rows has accepted 0; rows behind the last request's stay as
- * they are.  Rows that a broken q_start gives to two requests are written by both.  Probabilities that are NaN or negative
- * count as 0 in weights, and NaN never accepts.  Nothing waits for the host: the
- * call can be captured, and the rows of K/V behind the new length are
- * overwritten by the next append.
+ * they are.  Rows that a broken q_start gives to two requests are written by both.
+ * Probabilities that are NaN or negative count as 0 in weights, and NaN never
+ * accepts.  Arrays that are written have memory of their own: one that overlaps
+ * another of these arrays is an error (next_tokens == tokens too; rows of
+ * probabilities, which must not be overlapped either, are not compared).
+ * Nothing waits for the host: the call can be captured, and the rows of K/V behind
+ * the new length are overwritten by the next append.
  * Supported: vocab_size up to 2^20; rows need no alignment beyond their type's
  * (16-byte aligned rows are read in wider loads). */
 #define PFKV_REQ_BAD_TOKEN 0x4

@@ -337,7 +337,8 @@ def _positions(t, rotary: Rotary, tokens: int, device: int) -> int:
 def rotary_embed(out, x, positions, rotary: Rotary, stream=None):
     """Turn bf16 rows x [T][H][D] by their token's positions int32 [axes][T]
     ([T] for one axis) into out, which may be x itself.  Both may be parts of
-    wider rows (any stride between tokens that is a multiple of 8)."""
+    wider rows (any stride between tokens that is a multiple of 8), of the same
+    ones too where the parts lie beside each other."""
     import torch
     dev = x.get_device()
     T, H, D = x.shape
@@ -584,7 +585,8 @@ def verify_drafts(next_tokens, accepted, target_probs, draft_probs, tokens, unif
     or None where drafts were not sampled; tokens int32 [T]; uniforms float32
     [T] in [0, 1).  Rows of probabilities may lie further apart than V.
     context_lens: optional int32 [B] that loses the rejected tokens;
-    request_status: optional int32 [B]."""
+    request_status: optional int32 [B].  What is written overlaps no other
+    tensor of the call (tokens is not next_tokens)."""
     import torch
     dev = target_probs.get_device()
     T, V = target_probs.shape

@@ -21,6 +21,13 @@ int check_cuda(const char* what);
 
 inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
+// Whether two arrays (host view of their addresses) have bytes in common; none has
+// where it is NULL or empty.
+inline bool arrays_meet(const void* a, uint64_t a_bytes, const void* b, uint64_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return x && y && a_bytes && b_bytes && (x < y ? y - x < a_bytes : x - y < b_bytes);
+}
+
 // Number of SMs of the current device (queried each call; cheap).
 int device_sm_count();
 

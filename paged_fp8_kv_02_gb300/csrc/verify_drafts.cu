@@ -410,6 +410,17 @@ extern "C" int pfkv_verify_drafts(int32_t* next_tokens, int32_t* accepted, const
     return fail(PFKV_ERR_INVALID_ARG, "verify_drafts: rows are at least vocab_size elements apart");
   const int sms = device_sm_count();
   if (sms <= 0) return fail(PFKV_ERR_CUDA, "verify_drafts: no device");
+  // what is written has a place of its own: rows are shifted and lengths taken off by
+  // several CTAs, without an order between them
+  const struct {
+    const void* at;
+    uint64_t bytes;
+  } flat[] = {{next_tokens, 4ull * num_tokens}, {accepted, 4ull * batch},    {context_lens, 4ull * batch}, {request_status, 4ull * batch},
+              {tokens, 4ull * num_tokens},      {uniforms, 4ull * num_tokens}, {q_start, 4ull * batch + 4}};
+  for (int i = 0; i < 4; ++i)
+    for (int j = i + 1; j < 7; ++j)
+      if (arrays_meet(flat[i].at, flat[i].bytes, flat[j].at, flat[j].bytes))
+        return fail(PFKV_ERR_INVALID_ARG, "verify_drafts: an array that is written overlaps another one");
   // Powers of two up to what is resident at once, four CTAs per SM: 200 requests of
   // 50K words 17.3 us with clusters of 2, 20.0 of 3; 96 of 152K (bf16) 11.8 with 4,
   // 12.2 with 6, 16.7 with 8; at least 4096 words a CTA
