@@ -207,12 +207,13 @@ PFKV_API int pfkv_kv_append_fp8_block(const void *k_new, const void *v_new, void
  *     x' = x cos(phi) - y sin(phi),   y' = y cos(phi) + x sin(phi)
  * The pair is (first + i, first + num_pairs + i), or (first + 2i, first + 2i + 1)
  * where `neighbours` is set; channels outside [first, first + 2 num_pairs) stay.
- * A frequency is kept as the fraction of a turn per position in units of 2^-64,
- * so position times frequency wraps exactly in 64-bit integers: a far position
- * costs no more than the frequency's own rounding to double (2^-52 of the angle),
- * and a negative one turns back (as negative frequencies do: the gradient's turn).
- * Sine and cosine are fp32, off by little more than their rounding; pairs turn in
- * fp32 and are rounded once. */
+ * A frequency is kept as the fraction of a turn per position, cut to units of
+ * 2^-64, so position times frequency wraps exactly in 64-bit integers: the angle is
+ * off by at most |position| 2^-64 of a turn (2^-33 of one at the ends of 32 bits)
+ * and 2^-52 of itself (the division by 2 pi in double).  A negative position turns back (as negative frequencies do:
+ * the gradient's turn).  Sine and cosine are fp32, off by at most 0.65 2^-24 (a
+ * rounding to fp32 alone: 0.5 2^-24) whatever their size; pairs turn in fp32 and
+ * are rounded once. */
 #define PFKV_ROTARY_MAX_PAIRS 128
 #define PFKV_ROTARY_MAX_AXES 8
 /* Host description of a model's rotary positions, filled by pfkv_rotary_init
@@ -257,7 +258,8 @@ PFKV_API int pfkv_rotary_embed(void *out, int64_t out_stride, const void *x, int
  *   slot_mapping  int64 [num_tokens]; a token whose slot is < 0 or outside the
  *               cache is not appended; its query turns all the same
  *   granularity TENSOR, HEAD: scales are read.  TOKEN: written; the largest
- *               magnitude is taken after the turn (head_dim <= 512).  BLOCK:
+ *               magnitude is taken after the turn, in fp32, which a pair of
+ *               magnitude below 2^127 cannot leave (head_dim <= 512).  BLOCK:
  *               an error (rotary_embed, then kv_append_fp8_block).
  * q_out over k_new or v_new is an error, like q_out over q (in place, or parts of
  * the same wider rows, are none); a slot is named once.  Other arguments,
