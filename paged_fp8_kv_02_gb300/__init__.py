@@ -745,6 +745,9 @@ class PagePool:
         except Exception:
             pass
 
+    def __reduce_ex__(self, protocol):
+        raise TypeError("a PagePool is not copied or pickled: the copy would free the same pool")
+
     def num_free(self) -> int:
         return int(load().pfkv_pool_num_free(self._h))
 

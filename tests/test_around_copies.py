@@ -35,3 +35,12 @@ def test_a_changed_copy_leaves_the_original(pf):
     other = copy.deepcopy(first)
     other._struct.turns[0] = 0
     assert first._struct.turns[0] != 0 and first._ptr != other._ptr
+
+
+@pytest.mark.parametrize("how", [copy.copy, copy.deepcopy, pickle.dumps], ids=["copy", "deepcopy", "pickle"])
+def test_a_page_pool_is_not_copied(pf, how):
+    """Two objects of one pool would both free it."""
+    pool = pf.PagePool(4, 4)
+    with pytest.raises(TypeError):
+        how(pool)
+    assert pool.num_free() == 4
