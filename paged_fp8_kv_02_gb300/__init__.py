@@ -713,7 +713,7 @@ def copy_pages(arrays: PagedArrays, pairs, pair_status=None, stream=None):
     import torch
     dev = arrays.device
     n = pairs.shape[0]
-    _call("copy_pages", dev, stream, arrays._ptr, len(arrays.tensors), _want("pairs", pairs, torch.int32, (n, 2), dev), n,
+    _call("copy_pages", dev, stream, arrays._ptr, len(arrays._arrays), _want("pairs", pairs, torch.int32, (n, 2), dev), n,
           arrays.num_pages, None if pair_status is None else _want("pair_status", pair_status, torch.int32, (n,), dev))
 
 

@@ -44,3 +44,42 @@ def test_a_page_pool_is_not_copied(pf, how):
     with pytest.raises(TypeError):
         how(pool)
     assert pool.num_free() == 4
+
+
+def test_a_changed_list_of_tensors_changes_no_call(pf, monkeypatch):
+    """copy_pages passes as many descriptions as were made, whatever is done to
+    the list of tensors that keeps them alive."""
+    import torch
+
+    class Tensor:
+        shape, dtype, nbytes, device = (9, 64), torch.uint8, 9 * 64, "cuda:0"
+
+        def get_device(self):
+            return 0
+
+        def dim(self):
+            return 2
+
+        def is_contiguous(self):
+            return True
+
+        def data_ptr(self):
+            return 0x10000
+
+    class Pairs(Tensor):
+        shape, dtype = (1, 2), torch.int32
+
+    calls = []
+
+    class Lib:
+        def pfkv_copy_pages(self, *a):
+            calls.append(a)
+            return 0
+
+    monkeypatch.setattr(pf, "_lib", Lib())
+    monkeypatch.setattr(torch._C, "_cuda_getDevice", lambda: 0, raising=False)
+    monkeypatch.setattr(torch._C, "_cuda_getCurrentRawStream", lambda d: 0, raising=False)
+    arrays = pf.PagedArrays([Tensor(), Tensor()])
+    arrays.tensors.append(Tensor())
+    pf.copy_pages(arrays, Pairs())
+    assert calls[0][:2] == (ctypes.addressof(arrays._arrays), 2)
