@@ -4,8 +4,8 @@
 // of one page of one array (four 16-byte loads a lane, in flight together); K and V
 // pages, scales and bounds of every layer are units of the same list, so that one
 // launch takes a few small pages and many large ones alike.  1,361 pages of 64 KB in
-// two arrays, 357 MB: 52.8 us on the device, 6.76 TB/s, a plain copy's rate; 64 pages
-// of 16 KB in 64 arrays with their scales, 138 MB: 22.8; one page: 1.8.  4 KB a warp
+// two arrays, 357 MB: 52.9 us on the device, 6.74 TB/s, a plain copy's rate; 64 pages
+// of 16 KB in 64 arrays with their scales, 138 MB: 22.8; one page: 2.0.  4 KB a warp
 // in one go took 59.7 us of the first (fewer warps for the registers), stores without
 // the streaming policy 56.8, blocks of 256 threads 53.2.
 #include "pfkv_internal.h"

@@ -9,8 +9,8 @@
 //
 // Prompts are bounded by HBM (16,001 tokens, 64/8 heads of 128, scales per token, 624
 // MB: 105 us on the device, 5.9 TB/s, 88% of a plain copy's rate; 2,039 latent tokens
-// of 128 heads of 576, 605 MB: 100 us; 4,099 tokens of 48 query heads, 101 MB: 17.9
-// us).  A step of 64 tokens takes 3.5 us, queries alone 2.7: the launch and the chain
+// of 128 heads of 576, 605 MB: 101 us; 4,099 tokens of 48 query heads, 101 MB: 18.0
+// us).  A step of 64 tokens takes 3.6 us, queries alone 2.7: the launch and the chain
 // position -> angle -> turn -> store.  What the shape below gained: 168, 130, 23.3
 // and 3.9 us with a piece's place worked out for every row, the angles before the
 // first load and two CTAs per SM.
@@ -26,9 +26,10 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMaxTokens = 4;  // tokens a CTA takes at most
 // Query rows of a thread that are in flight together, and CTAs of an SM (64 registers
-// at four).  Prompt of 16,001 and 4,099 tokens, us (with sincospif): 2 rows at 4 CTAs 105.3 and 17.4, 3
-// at 4 104.5 and 18.2, 4 at 3 104.0 and 19.8, 4 at 4 111.0 and 20.2, 2 at 5
-// 111.1 and 20.3.
+// at four; rows of 128 with scales per token then spill one).  Prompt of 16,001 and
+// 4,099 tokens, us, with an earlier form of the angles (sincospif): 2 rows at 4 CTAs
+// 105.3 and 17.4, 3 at 4 104.5 and 18.2, 4 at 3 104.0 and 19.8, 4 at 4 111.0 and
+// 20.2, 2 at 5 111.1 and 20.3.
 constexpr int kBatch = 2;
 constexpr int kBlocks = 4;
 
@@ -342,10 +343,17 @@ int launch(const char* fn, RotaryArgs& a, bool token, cudaStream_t stream) {
     for (a.pitch = 1; a.pitch < pieces;) a.pitch *= 2;
   const int sms = device_sm_count();
   if (sms <= 0) return fail(PFKV_ERR_CUDA, "%s: no device", fn);
-  // Four tokens a CTA while that leaves two waves of CTAs and a row is no wider than
+  // A step's tokens are a CTA each, more than one where there are fewer than SMs.
+  // Two tokens a CTA from four an SM on, four from eight, where a row is no wider than
   // a quarter of a token's threads (36 pieces of a latent row leave 28 of 64 idle, 4
-  // of 256); eight take 113 us where four take 105.  A step's tokens are a CTA each,
-  // more than one where there are fewer than SMs.
+  // of 256).  us with 1, 2 and 4 of them on 152 SMs:
+  //   append, 64/8 heads of 128: 500 tokens 5.4 5.8 7.8, 608 5.9 6.2 8.3, 700 8.8 7.1
+  //   9.2, 1,216 10.9 8.9 11.4, 2,432 20.3 17.7 18.8, 8,000 60 53.5 55.6, 16,001 with
+  //   scales per token 120.6 105.3 105.8 (8: 113, with an earlier form of the angles)
+  //   queries alone, 48 heads: 608 4.1 4.5 4.7, 1,216 7.6 7.5 7.6, 2,432 13.0 12.6
+  //   11.6, 4,099 19.5 19.0 18.0, 16,001 67.2 62.7 59.2
+  // One rule serves both: the append alone would do with two (2.4 us less at 1,216
+  // tokens, 4% at 8,000).
   int tokens = kMaxTokens;
   while (tokens > 1 && (a.T < 2 * sms * tokens || a.pitch * 4 > kThreads / tokens)) tokens /= 2;
   int parts = 1;

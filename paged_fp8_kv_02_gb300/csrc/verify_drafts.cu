@@ -10,12 +10,14 @@
 // memory, and the CTA that holds the threshold reads one block again to find the
 // token.
 //
-// 64 requests with up to seven drafts, 128,259 words in fp32 (62 MB): 13.5 us on the
-// device, of which the launch, the chain lengths -> token -> probability in front of
-// the row, the exchange and the block take about 6; 96 with up to five looked-up
-// drafts, 152,064 words in bf16 (29 MB): 11.4; one of 32,768 words: 4.5.  Word by word
-// and with conversions to 64-bit integers these took 25.0, 65.5 and 6.0 us; reading a
-// warp's whole part again for the token 14.1, 13.3 and 4.5.
+// 64 requests with up to seven drafts, 128,259 words in fp32 (62 MB): 13.7 us on the
+// device; 96 with up to five looked-up drafts, 152,064 words in bf16 (29 MB): 11.6; one
+// of 32,768 words: 4.8.  What bounds them: launch, the chain lengths -> token ->
+// probability in front of the row and the exchange (a request alone has little else),
+// then a warp's blocks one after the other, a trip to memory each (one request: 4.8
+// us at 32,768 words, a block a warp, 6.3 at 128,259, four), and HBM last.  Word by
+// word and with conversions to 64-bit integers these took 25.0, 65.5 and 6.0 us;
+// reading a warp's whole part again for the token 14.1, 13.3 and 4.5.
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -258,7 +260,9 @@ __global__ void __launch_bounds__(kThreads, 1024 / kThreads) verify_drafts_kerne
   int shift, places, block, part;
   uint64_t total = 0, before = 0;
   for (int pass = 0;; ++pass) {
-    // where the two rows stand alike within 16 bytes they are read 16 bytes at a time
+    // where the two rows stand alike within 16 bytes they are read 16 bytes at a time,
+    // else word by word (64 requests of 128,259 words: 13.5 us either way in fp32, 10.9
+    // and 12.8 in bf16)
     const int p_at = (int)(reinterpret_cast<uintptr_t>(row.p) & 15), q_at = (int)(reinterpret_cast<uintptr_t>(row.q) & 15);
     const bool wide = !row.q || p_at == q_at;
     shift = wide ? p_at / (int)sizeof(T) : 0;
@@ -421,9 +425,11 @@ extern "C" int pfkv_verify_drafts(int32_t* next_tokens, int32_t* accepted, const
     for (int j = i + 1; j < 7; ++j)
       if (arrays_meet(flat[i].at, flat[i].bytes, flat[j].at, flat[j].bytes))
         return fail(PFKV_ERR_INVALID_ARG, "verify_drafts: an array that is written overlaps another one");
-  // Powers of two up to what is resident at once, four CTAs per SM: 200 requests of
-  // 50K words 17.3 us with clusters of 2, 20.0 of 3; 96 of 152K (bf16) 11.8 with 4,
-  // 12.2 with 6, 16.7 with 8; at least 4096 words a CTA
+  // Powers of two up to what is resident at once, four CTAs per SM, while a CTA is left
+  // with more than 2048 words.  us with clusters of 1, 2, 4 and 8 on 152 SMs: 20
+  // requests of 20,000 words 7.1 6.0 5.7 5.3 (taken: 8), 64 of 128,259 32 20.0 14.7
+  // 13.8 (8), 96 of 152,064 (bf16, looked up) 19.9 14.9 12.0 17.2 (4), 150 of 32,768
+  // 12.5 10.0 11.7 14.3 (4), 200 of 50,000 18.3 15.2 19.0 21.2 (2)
   int cluster = kMaxCluster;
   while (cluster > 1 && (int64_t)batch * cluster > 4 * sms) cluster /= 2;
   while (cluster > 1 && vocab_size <= 4096 * (cluster / 2)) cluster /= 2;
