@@ -820,7 +820,8 @@ PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages
  *   pairs        int32 [num_pairs][2] (device): source, destination.  A pair
  *                with a negative entry is padding.
  *   pair_status  optional int32 [num_pairs], written: 0, or PFKV_DEVERR_BAD_PAGE
- *                for a pair that names a page >= num_pages (not copied)
+ *                for a pair that names a page >= num_pages (not copied).  Over
+ *                the pairs it is an error
  * A page may be the source of many pairs.  A page that is the destination of
  * two pairs, or the destination of one and the source of another, ends with
  * unspecified bytes of the pages involved (the copies run at the same time).

@@ -107,6 +107,8 @@ extern "C" int pfkv_copy_pages(const pfkv_paged_array* arrays, int num_arrays, c
   if (num_pairs == 0 || num_arrays == 0) return PFKV_OK;
   if (!pairs || !aligned(pairs, 8) || (pair_status && !aligned(pair_status, 4)))
     return fail(PFKV_ERR_INVALID_ARG, "copy_pages: null or misaligned pointer (pairs start on 8 bytes)");
+  if (arrays_meet(pairs, 8ull * num_pairs, pair_status, 4ull * num_pairs))
+    return fail(PFKV_ERR_INVALID_ARG, "copy_pages: pair_status overlaps pairs");
   cudaStream_t s = reinterpret_cast<cudaStream_t>(stream);
   CopyArgs a;
   a.pairs = reinterpret_cast<const int2*>(pairs);
