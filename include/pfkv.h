@@ -241,7 +241,8 @@ PFKV_API int pfkv_rotary_init(pfkv_rotary *rotary, const double *frequencies, co
  *   positions   int32 [num_axes][num_tokens]
  * For caches that rotary_append_fp8 does not fill: turned keys go on to
  * kv_append_fp8_block or kv_append_bf16.  Supported: head_dim a multiple of 16
- * up to 4096 with first + 2 num_pairs <= head_dim. */
+ * up to 4096 with first + 2 num_pairs <= head_dim, rows of fewer than 2^30
+ * channels (rotary_append_fp8: queries, keys and values together). */
 PFKV_API int pfkv_rotary_embed(void *out, int64_t out_stride, const void *x, int64_t x_stride,
                                const int32_t *positions, const pfkv_rotary *rotary, int num_tokens,
                                int num_heads, int head_dim, pfkv_stream_t stream);
@@ -617,8 +618,8 @@ PFKV_API int pfkv_paged_prefill_attn(void *out, const void *q, const void *k_cac
  * probabilities, which must not be overlapped either, are not compared).
  * Nothing waits for the host: the call can be captured, and the rows of K/V behind
  * the new length are overwritten by the next append.
- * Supported: vocab_size up to 2^20; rows need no alignment beyond their type's
- * (16-byte aligned rows are read in wider loads). */
+ * Supported: vocab_size up to 2^20, batch up to 2^24; rows need no alignment
+ * beyond their type's (16-byte aligned rows are read in wider loads). */
 #define PFKV_REQ_BAD_TOKEN 0x4
 #define PFKV_REQ_NO_MASS 0x8
 typedef enum { PFKV_PROB_F32 = 0, PFKV_PROB_BF16 = 1, PFKV_PROB_F16 = 2 } pfkv_prob_dtype;
@@ -817,8 +818,8 @@ PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages
  *                K, V, scales, bounds, latents of any number of layers, each
  *                num_pages pages of page_bytes bytes, page_stride bytes apart
  *                (>= page_bytes)
- *   pairs        int32 [num_pairs][2] (device): source, destination.  A pair
- *                with a negative entry is padding.
+ *   pairs        int32 [num_pairs][2] (device, starting on 8 bytes): source,
+ *                destination.  A pair with a negative entry is padding.
  *   pair_status  optional int32 [num_pairs], written: 0, or PFKV_DEVERR_BAD_PAGE
  *                for a pair that names a page >= num_pages (not copied).  Over
  *                the pairs it is an error
@@ -834,8 +835,7 @@ PFKV_API int pfkv_slots_from_table(const int32_t *block_table_row, int max_pages
  * next fork's source).
  * Any alignment and size; pages and strides that are multiples of 16 bytes are
  * the fast ones.  No pairs or no arrays: nothing is enqueued.  Supported:
- * page_bytes < 2^31; arrays beyond 128 take another
- * launch each 128. */
+ * page_bytes < 2^31; arrays beyond 128 take another launch each 128. */
 typedef struct {
   void *base;
   int64_t page_bytes, page_stride;

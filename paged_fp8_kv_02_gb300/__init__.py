@@ -704,7 +704,7 @@ class PagedArrays:
 
 def copy_pages(arrays: PagedArrays, pairs, pair_status=None, stream=None):
     """Copy page pairs[i][0] to page pairs[i][1] in every array (pairs int32
-    [n][2]; a pair with a negative entry is padding).  No page may be the
+    [n][2] on 8 bytes; a pair with a negative entry is padding).  No page may be the
     destination of two pairs, or of one and the source of another: its bytes
     are unspecified then.  The pairs of one PagePool.compact, or of
     make_writable calls without a fork, a cut, a release or a compact between
