@@ -46,8 +46,8 @@ def test_queries_over_keys_or_values_are_refused():
         wide = dict(q=far, qs=1536, qo=far, qos=1536, k=far + 2048, ks=1536, v=far + 2560, vs=1536)
         expect(append, NO, **wide)
         expect(append, BAD, **dict(wide, **{kv: far + 2048 - 256}))
-        expect(append, BAD, **dict(wide, **{kv: far + 3072 - 256}))     # the next token's first head
-        expect(append, NO, **dict(wide, T=1, **{kv: far + 3072 - 256}))
+        expect(append, BAD, **dict(wide, **{kv: far + 2 * 1536 - 256}))     # the next token's first head
+        expect(append, NO, **dict(wide, T=1, **{kv: far + 2 * 1536 - 256}))
         expect(append, BAD, **dict(wide, T=1, **{kv: far + 2048 - 256}))
         expect(append, BAD, **dict(wide, **{step: 1544}))   # another stride: by extents
         expect(append, NO, **dict(wide, T=1, **{step: 1544}))
